@@ -497,6 +497,181 @@ int zero_gather_dequant(const zero_plan* plan, const void* const* code_shards,
                         void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* 8-bit activation checkpoints                                            */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * What a training step keeps between its forward and backward pass besides
+ * the model state is activations: a checkpointed activation is stored in the
+ * forward and read again in the backward pass (L18 notes §4.1, §4.2).  These
+ * calls store it in 8 bits, compute the layers' backward passes from the
+ * 8-bit form, and write the weight gradients in 16 bits where the reduce
+ * reads them (zero_reduce_shard's contributions).
+ *
+ * Checkpoint of a [rows, cols] matrix of 16-bit values: blocks of ZERO_QBLOCK
+ * consecutive elements of a row (a row's last block may be short) with one
+ * fp32 scale each,
+ *   ZERO_ACT_INT8  scale = max|x| / 127; code = round_half_even(x / scale),
+ *                  int8, clamped to [-127, 127]
+ *   ZERO_ACT_E4M3  scale = max|x| / 448; code = x / scale rounded to nearest
+ *                  even in 4 exponent and 3 mantissa bits (largest value 448,
+ *                  no infinities), clamped to [-448, 448]
+ * with IEEE fp32 divisions.  Restored value = round_to_nearest_even_16(fp32(
+ * code * scale)); a backward pass computes with these 16-bit values, so it
+ * gives what the ordinary backward pass gives on the restored activation.  A
+ * block of zeros has scale 0.  A block that holds an infinity or NaN has scale
+ * NaN and codes 0: all of it is restored as NaN, so a non-finite activation
+ * reaches the gradient and its flag instead of turning finite.
+ *
+ * Layout: codes, one byte per element, rows ceil(cols / 16) * 16 bytes apart
+ * (the pad bytes are written as 0), 16-byte aligned; scales, fp32,
+ * [rows, ceil(cols / ZERO_QBLOCK)].  Rows are independent: rows r0.. of a
+ * checkpoint are a checkpoint that starts r0 rows into codes and scales, so
+ * a rank that keeps or receives a range of rows (partitioned activation
+ * checkpoints, L18 notes §4.2) passes those pointers.
+ *
+ * Matrices of 16-bit values: `stride` elements from row to row (>= cols), 2-byte
+ * aligned; columns are adjacent.  Two matrices of one call with the same
+ * stride may interleave (the halves of one product's output); otherwise
+ * outputs may not overlap each other or an input (ZERO_EALIAS), except where a
+ * call says so.  `dtype` is that of every 16-bit array of the call.
+ * 0 <= rows, 0 <= cols <= ZERO_ACT_MAX_COLS, and rows * (cols rounded up to
+ * ZERO_QBLOCK) <= ZERO_MAX_ELEMS.  Sums are fp32 in an order that depends only on the sizes,
+ * so results are bitwise repeatable.  Nothing is allocated, copied to the
+ * host or recorded as a memset: every call can be captured in a HIP graph.
+ */
+#define ZERO_ACT_INT8 1
+#define ZERO_ACT_E4M3 2
+#define ZERO_ACT_MAX_COLS (INT64_C(1) << 30)
+
+/* Code bytes and number of fp32 scales of a checkpoint; -1 on bad arguments. */
+int64_t zero_act_code_bytes(int64_t rows, int64_t cols);
+int64_t zero_act_scale_count(int64_t rows, int64_t cols);
+
+/* zero_act_save -- writes the checkpoint of x.  For cols a multiple of
+ * ZERO_QBLOCK and x_stride = cols, the ZERO_ACT_INT8 codes and scales of
+ * finite values are those of zero_quantize_blocks. */
+int zero_act_save(const void* x, int64_t x_stride, int dtype, int64_t rows, int64_t cols,
+                  int format, void* codes, float* scales, void* stream);
+
+/* zero_act_restore -- reads a checkpoint back into 16 bits (any 16-bit dtype,
+ * not only the saved one). */
+int zero_act_restore(const void* codes, const float* scales, int format, int64_t rows,
+                     int64_t cols, void* y, int64_t y_stride, int dtype, void* stream);
+
+/* The activation function f of the gated-activation calls. */
+#define ZERO_GLU_SILU 1      /* f(g) = g / (1 + exp(-g)) */
+#define ZERO_GLU_GELU 2      /* f(g) = g * (1 + erf(g / sqrt(2))) / 2 */
+#define ZERO_GLU_GELU_TANH 3 /* f(g) = g * (1 + tanh(sqrt(2/pi) * (g + 0.044715 g^3))) / 2 */
+
+/*
+ * zero_act_glu_forward -- an MLP's (gated) activation with the checkpoints of
+ * its inputs, in one pass:
+ *   h = round16(f(gate) * up), or round16(f(gate)) if up is NULL
+ * evaluated in fp32 from the 16-bit inputs, and the checkpoint of gate and (if
+ * up is given; otherwise up_codes and up_scales must be NULL) of up.  gate and
+ * up may be the halves of one matrix.  Errors: ZERO_EINVAL, ZERO_EALIAS,
+ * ZERO_EHIP.
+ */
+int zero_act_glu_forward(const void* gate, int64_t gate_stride, const void* up, int64_t up_stride,
+                         int dtype, int64_t rows, int64_t cols, int fn, int format, void* h,
+                         int64_t h_stride, void* gate_codes, float* gate_scales, void* up_codes,
+                         float* up_scales, void* stream);
+
+/*
+ * zero_act_glu_backward -- its backward pass from the checkpoints, with g and
+ * u the restored gate and up (u = 1 without up):
+ *   dgate = round16(dh * u * f'(g)),   dup = round16(dh * f(g))
+ *   h     = round16(f(g) * u)          (if h is not NULL: the activation again,
+ *                                       for the next product's weight gradient)
+ * up_codes, up_scales and dup are given together or all NULL.
+ */
+int zero_act_glu_backward(const void* gate_codes, const float* gate_scales, const void* up_codes,
+                          const float* up_scales, int format, int64_t rows, int64_t cols, int fn,
+                          const void* dh, int64_t dh_stride, int dtype, void* dgate,
+                          int64_t dgate_stride, void* dup, int64_t dup_stride, void* h,
+                          int64_t h_stride, void* stream);
+
+/* The norm of the residual calls, over the columns of a row. */
+#define ZERO_NORM_RMS 1   /* n = r / sqrt(mean(r^2) + eps) */
+#define ZERO_NORM_LAYER 2 /* n = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) */
+
+/* Longest row of the norm calls (a row stays in registers). */
+#define ZERO_NORM_MAX_COLS 16384
+
+/*
+ * zero_act_norm_forward -- a block's output added to the residual stream, the
+ * norm that the next block starts with, and the checkpoint of the stream:
+ *   res = round16(x + alpha * branch)  (fp32: the product rounded, then the
+ *                                       sum); res = x if branch is NULL
+ *   y   = round16(n(res) * weight + bias)
+ * with the statistics taken from the 16-bit res in fp32.  rstd[row] =
+ * 1 / sqrt(.. + eps), and for ZERO_NORM_LAYER mean[row], are kept for the
+ * backward pass; codes and scales receive the checkpoint of res.
+ *
+ * branch NULL: res must be NULL too and alpha is ignored.  res may be exactly
+ * x (same pointer and stride: the stream updated in place).  weight, bias:
+ * `cols` 16-bit values each, or NULL (1 and 0).  mean: fp32, NULL for
+ * ZERO_NORM_RMS.  eps > 0, alpha finite.  cols <= ZERO_NORM_MAX_COLS.
+ */
+int zero_act_norm_forward(const void* x, int64_t x_stride, const void* branch,
+                          int64_t branch_stride, float alpha, const void* weight, const void* bias,
+                          int dtype, int64_t rows, int64_t cols, int kind, float eps, int format,
+                          void* res, int64_t res_stride, void* y, int64_t y_stride, void* codes,
+                          float* scales, float* mean, float* rstd, void* stream);
+
+/* Device workspace of zero_act_norm_backward (for the sums over rows); -1 on
+ * bad arguments. */
+int64_t zero_act_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * zero_act_norm_backward -- its backward pass from the checkpoint.  With r the
+ * restored res, n = (r - mean) * rstd, d = dy * weight:
+ *   dr      = rstd * (d - n * mean(d * n) [- mean(d) for ZERO_NORM_LAYER]) + dres
+ *   dx      = round16(dr),  dbranch = round16(alpha * dr)
+ *   dweight = round16(sum over rows of dy * n  [+ dweight if accumulate])
+ *   dbias   = round16(sum over rows of dy      [+ dbias if accumulate])
+ * dres: the gradient that arrives along the residual stream, or NULL (0); dx
+ * may be exactly dres (same pointer and stride).  dbranch, dweight and dbias
+ * may each be NULL (not wanted; alpha is ignored without dbranch).  dweight
+ * and dbias are `cols` 16-bit values at any 2-byte offset, typically the
+ * tensors' places in the rank's local gradient.  workspace: >=
+ * zero_act_norm_workspace_bytes(rows, cols), 16-byte aligned; may be NULL if
+ * neither dweight nor dbias is wanted.  rows = 0 writes dweight and dbias
+ * (zero, or unchanged if accumulating).
+ */
+int zero_act_norm_backward(const void* codes, const float* scales, int format, const float* mean,
+                           const float* rstd, const void* weight, int64_t rows, int64_t cols,
+                           int kind, const void* dy, int64_t dy_stride, const void* dres,
+                           int64_t dres_stride, float alpha, int dtype, void* dx, int64_t dx_stride,
+                           void* dbranch, int64_t dbranch_stride, int accumulate, void* dweight,
+                           void* dbias, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Device workspace of zero_act_weight_grad; -1 on bad arguments. */
+int64_t zero_act_weight_grad_workspace_bytes(int64_t rows, int64_t in_cols, int64_t out_cols);
+
+/*
+ * zero_act_weight_grad -- the weight gradient of a linear layer y = x W^T + b
+ * from the checkpoint of its input x (rows tokens of in_cols) and the
+ * gradient dy (rows tokens of out_cols) of its output, with x the restored
+ * 16-bit values:
+ *   dweight[o, i] = round16(sum over t of dy[t, o] * x[t, i]  [+ dweight[o, i]])
+ *   dbias[o]      = round16(sum over t of dy[t, o]            [+ dbias[o]])
+ * (the bracketed terms if accumulate != 0: gradients of several micro-batches
+ * add up).  Products are exact, sums fp32.  dweight is [out_cols, in_cols]
+ * without gaps at any 2-byte offset, typically the tensor's place in the
+ * rank's local gradient; dbias is out_cols values or NULL.  workspace: >=
+ * zero_act_weight_grad_workspace_bytes(rows, in_cols, out_cols), 16-byte
+ * aligned (NULL if that is 0).  rows = 0 writes zeros, or nothing if
+ * accumulating.  in_cols, out_cols: each with rows within the limit above,
+ * and in_cols * out_cols <= ZERO_MAX_ELEMS.
+ */
+int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const void* codes,
+                         const float* scales, int format, int64_t rows, int64_t in_cols,
+                         int64_t out_cols, int accumulate, void* dweight, void* dbias,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Sharded checkpoints and restoring under another partition               */
 /* ---------------------------------------------------------------------- */
 

@@ -43,6 +43,9 @@ EXPORTED = (
     "zero_plan_reshard", "zero_ckpt_save", "zero_ckpt_load", "zero_adam_consts_fill", "zero_adam_step_consts",
     "zero_grad_norm_noalloc", "zero_reduce_owners", "zero_adam_step_owners", "zero_step_end",
     "zero_offload_create", "zero_offload_destroy", "zero_offload_begin", "zero_offload_end",
+    "zero_act_code_bytes", "zero_act_scale_count", "zero_act_save", "zero_act_restore", "zero_act_glu_forward",
+    "zero_act_glu_backward", "zero_act_norm_forward", "zero_act_norm_workspace_bytes", "zero_act_norm_backward",
+    "zero_act_weight_grad_workspace_bytes", "zero_act_weight_grad",
 )
 ZERO_QBLOCK = 256
 ZERO_CPU_SCALAR = 0
@@ -54,6 +57,15 @@ ZERO_LOC_HOST = 1
 ZERO_CKPT_BLOCK = 262144
 ZERO_CKPT_MIN_STAGING = 2 * 4 * ZERO_CKPT_BLOCK
 ZERO_NOALLOC_MAX_ELEMS = 1 << 34
+ZERO_ACT_INT8 = 1
+ZERO_ACT_E4M3 = 2
+ZERO_ACT_MAX_COLS = 1 << 30
+ZERO_GLU_SILU = 1
+ZERO_GLU_GELU = 2
+ZERO_GLU_GELU_TANH = 3
+ZERO_NORM_RMS = 1
+ZERO_NORM_LAYER = 2
+ZERO_NORM_MAX_COLS = 16384
 ZERO_NOALLOC_SCRATCH_BYTES = 16384 + 8 * (ZERO_NOALLOC_MAX_ELEMS // 2048)
 
 
@@ -145,6 +157,20 @@ _sig = {
     "zero_ckpt_save": (_I, [ctypes.c_char_p, _P, _I, _I64, _P, _P, _P, _I, _P, _I64, _P]),
     "zero_ckpt_load": (_I, [ctypes.POINTER(ctypes.c_char_p), _I, _P, _I, _P, _P, _P, _I, ctypes.POINTER(_I64), _P,
                             _I64, _P]),
+    "zero_act_code_bytes": (_I64, [_I64, _I64]),
+    "zero_act_scale_count": (_I64, [_I64, _I64]),
+    "zero_act_save": (_I, [_P, _I64, _I, _I64, _I64, _I, _P, _P, _P]),
+    "zero_act_restore": (_I, [_P, _P, _I, _I64, _I64, _P, _I64, _I, _P]),
+    "zero_act_glu_forward": (_I, [_P, _I64, _P, _I64, _I, _I64, _I64, _I, _I, _P, _I64, _P, _P, _P, _P, _P]),
+    "zero_act_glu_backward": (_I, [_P, _P, _P, _P, _I, _I64, _I64, _I, _P, _I64, _I, _P, _I64, _P, _I64, _P, _I64,
+                                   _P]),
+    "zero_act_norm_forward": (_I, [_P, _I64, _P, _I64, ctypes.c_float, _P, _P, _I, _I64, _I64, _I, ctypes.c_float, _I,
+                                   _P, _I64, _P, _I64, _P, _P, _P, _P, _P]),
+    "zero_act_norm_workspace_bytes": (_I64, [_I64, _I64]),
+    "zero_act_norm_backward": (_I, [_P, _P, _I, _P, _P, _P, _I64, _I64, _I, _P, _I64, _P, _I64, ctypes.c_float, _I,
+                                    _P, _I64, _P, _I64, _I, _P, _P, _P, _I64, _P]),
+    "zero_act_weight_grad_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "zero_act_weight_grad": (_I, [_P, _I64, _I, _P, _P, _I, _I64, _I64, _I64, _I, _P, _P, _P, _I64, _P]),
     "zero_cpu_isa": (_I, []),
     "zero_cpu_set_isa": (_I, [_I]),
     "zero_last_error": (ctypes.c_char_p, []),
@@ -547,6 +573,167 @@ def zero_gather_dequant(plan, code_shards, scale_shards, unit_begin, unit_end, b
     sp = _table(scale_shards, scale_bytes, "scale shard")
     _check(lib.zero_gather_dequant(handle, cp, sp, int(unit_begin), int(unit_end), int(bits), _dtype(dtype),
                                    _ptr(full), _ptr(workspace), wb, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit activation checkpoints
+# ---------------------------------------------------------------------------
+
+def _need_here(x, nbytes, what):
+    """_need, and on the current device (the call's stream belongs to it)."""
+    if x is None or isinstance(x, int) or nbytes <= 0:
+        return
+    _need(x, nbytes, what)
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on device {x.device.index}, the current one is {torch.cuda.current_device()}")
+
+
+def _need_matrix(x, rows, cols, stride, what):
+    """A tensor argument must be a 16-bit device matrix whose memory holds `rows` rows of `cols` adjacent
+    values, `stride` apart (a view into a larger matrix will do)."""
+    if x is None or isinstance(x, int) or rows <= 0 or cols <= 0:
+        return
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on device {x.device.index}, the current one is {torch.cuda.current_device()}")
+    if x.element_size() != 2:
+        raise ValueError(f"{what} must hold 16-bit values")
+    if x.dim() > 0 and x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{what}'s columns must be adjacent")
+    if x.dim() == 2 and x.shape[0] > 1 and x.stride(0) != stride:
+        raise ValueError(f"{what}'s rows are {x.stride(0)} apart, not {stride}")
+    have = x.untyped_storage().nbytes() // 2 - x.storage_offset()
+    need = (rows - 1) * stride + cols
+    if have < need:
+        raise ValueError(f"{what} holds {have} values, needs {need}")
+
+
+def _need_checkpoint(codes, scales, rows, cols, what=""):
+    # sizes out of range are the library's to report
+    pitch = (cols + 15) // 16 * 16
+    _need_here(codes, rows * pitch, f"{what}codes")
+    _need_here(scales, 4 * rows * ((cols + ZERO_QBLOCK - 1) // ZERO_QBLOCK), f"{what}scales")
+
+
+def zero_act_code_bytes(rows, cols):
+    b = lib.zero_act_code_bytes(int(rows), int(cols))
+    if b < 0:
+        raise ZeroError(ZERO_EINVAL, zero_last_error())
+    return b
+
+
+def zero_act_scale_count(rows, cols):
+    c = lib.zero_act_scale_count(int(rows), int(cols))
+    if c < 0:
+        raise ZeroError(ZERO_EINVAL, zero_last_error())
+    return c
+
+
+def zero_act_save(x, x_stride, dtype, rows, cols, format, codes, scales, stream=None):
+    _need_matrix(x, rows, cols, x_stride, "x")
+    _need_checkpoint(codes, scales, rows, cols)
+    _check(lib.zero_act_save(_ptr(x), int(x_stride), _dtype(dtype), int(rows), int(cols), int(format), _ptr(codes),
+                             _ptr(scales), _stream(stream)))
+
+
+def zero_act_restore(codes, scales, format, rows, cols, y, y_stride, dtype, stream=None):
+    _need_checkpoint(codes, scales, rows, cols)
+    _need_matrix(y, rows, cols, y_stride, "y")
+    _check(lib.zero_act_restore(_ptr(codes), _ptr(scales), int(format), int(rows), int(cols), _ptr(y), int(y_stride),
+                                _dtype(dtype), _stream(stream)))
+
+
+def zero_act_glu_forward(gate, gate_stride, up, up_stride, dtype, rows, cols, fn, format, h, h_stride, gate_codes,
+                         gate_scales, up_codes, up_scales, stream=None):
+    _need_matrix(gate, rows, cols, gate_stride, "gate")
+    _need_matrix(up, rows, cols, up_stride, "up")
+    _need_matrix(h, rows, cols, h_stride, "h")
+    _need_checkpoint(gate_codes, gate_scales, rows, cols, "gate_")
+    _need_checkpoint(up_codes, up_scales, rows, cols, "up_")
+    _check(lib.zero_act_glu_forward(_ptr(gate), int(gate_stride), _ptr(up), int(up_stride), _dtype(dtype), int(rows),
+                                    int(cols), int(fn), int(format), _ptr(h), int(h_stride), _ptr(gate_codes),
+                                    _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), _stream(stream)))
+
+
+def zero_act_glu_backward(gate_codes, gate_scales, up_codes, up_scales, format, rows, cols, fn, dh, dh_stride, dtype,
+                          dgate, dgate_stride, dup, dup_stride, h=None, h_stride=0, stream=None):
+    _need_checkpoint(gate_codes, gate_scales, rows, cols, "gate_")
+    _need_checkpoint(up_codes, up_scales, rows, cols, "up_")
+    _need_matrix(dh, rows, cols, dh_stride, "dh")
+    _need_matrix(dgate, rows, cols, dgate_stride, "dgate")
+    _need_matrix(dup, rows, cols, dup_stride, "dup")
+    _need_matrix(h, rows, cols, h_stride, "h")
+    _check(lib.zero_act_glu_backward(_ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), int(format),
+                                     int(rows), int(cols), int(fn), _ptr(dh), int(dh_stride), _dtype(dtype),
+                                     _ptr(dgate), int(dgate_stride), _ptr(dup), int(dup_stride), _ptr(h),
+                                     int(h_stride), _stream(stream)))
+
+
+def zero_act_norm_forward(x, x_stride, branch, branch_stride, alpha, weight, bias, dtype, rows, cols, kind, eps, format,
+                          res, res_stride, y, y_stride, codes, scales, mean, rstd, stream=None):
+    _need_matrix(x, rows, cols, x_stride, "x")
+    _need_matrix(branch, rows, cols, branch_stride, "branch")
+    _need_matrix(res, rows, cols, res_stride, "res")
+    _need_matrix(y, rows, cols, y_stride, "y")
+    _need_checkpoint(codes, scales, rows, cols)
+    if rows > 0:
+        _need_here(weight, 2 * cols, "weight")
+        _need_here(bias, 2 * cols, "bias")
+    _need_here(mean, 4 * rows, "mean")
+    _need_here(rstd, 4 * rows, "rstd")
+    _check(lib.zero_act_norm_forward(_ptr(x), int(x_stride), _ptr(branch), int(branch_stride), float(alpha),
+                                     _ptr(weight), _ptr(bias), _dtype(dtype), int(rows), int(cols), int(kind),
+                                     float(eps), int(format), _ptr(res), int(res_stride), _ptr(y), int(y_stride),
+                                     _ptr(codes), _ptr(scales), _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def zero_act_norm_workspace_bytes(rows, cols):
+    b = lib.zero_act_norm_workspace_bytes(int(rows), int(cols))
+    if b < 0:
+        raise ZeroError(ZERO_EINVAL, zero_last_error())
+    return b
+
+
+def zero_act_norm_backward(codes, scales, format, mean, rstd, weight, rows, cols, kind, dy, dy_stride, dres,
+                           dres_stride, alpha, dtype, dx, dx_stride, dbranch, dbranch_stride, accumulate, dweight,
+                           dbias, workspace, stream=None, workspace_bytes=None):
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _need_checkpoint(codes, scales, rows, cols)
+    _need_here(mean, 4 * rows, "mean")
+    _need_here(rstd, 4 * rows, "rstd")
+    _need_here(weight, 2 * cols, "weight")
+    for t, stride, what in ((dy, dy_stride, "dy"), (dres, dres_stride, "dres"), (dx, dx_stride, "dx"),
+                            (dbranch, dbranch_stride, "dbranch")):
+        _need_matrix(t, rows, cols, stride, what)
+    _need_here(dweight, 2 * cols, "dweight")
+    _need_here(dbias, 2 * cols, "dbias")
+    _need_here(workspace, wb, "workspace")
+    _check(lib.zero_act_norm_backward(_ptr(codes), _ptr(scales), int(format), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                      int(rows), int(cols), int(kind), _ptr(dy), int(dy_stride), _ptr(dres),
+                                      int(dres_stride), float(alpha), _dtype(dtype), _ptr(dx), int(dx_stride),
+                                      _ptr(dbranch), int(dbranch_stride), int(bool(accumulate)), _ptr(dweight),
+                                      _ptr(dbias), _ptr(workspace), wb, _stream(stream)))
+
+
+def zero_act_weight_grad_workspace_bytes(rows, in_cols, out_cols):
+    b = lib.zero_act_weight_grad_workspace_bytes(int(rows), int(in_cols), int(out_cols))
+    if b < 0:
+        raise ZeroError(ZERO_EINVAL, zero_last_error())
+    return b
+
+
+def zero_act_weight_grad(dy, dy_stride, dtype, codes, scales, format, rows, in_cols, out_cols, accumulate, dweight,
+                         dbias, workspace, stream=None, workspace_bytes=None):
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _need_matrix(dy, rows, out_cols, dy_stride, "dy")
+    _need_checkpoint(codes, scales, rows, in_cols)
+    _need_here(dweight, 2 * in_cols * out_cols, "dweight")
+    _need_here(dbias, 2 * out_cols, "dbias")
+    _need_here(workspace, wb, "workspace")
+    _check(lib.zero_act_weight_grad(_ptr(dy), int(dy_stride), _dtype(dtype), _ptr(codes), _ptr(scales), int(format),
+                                    int(rows), int(in_cols), int(out_cols), int(bool(accumulate)), _ptr(dweight),
+                                    _ptr(dbias), _ptr(workspace), wb, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -56,7 +56,7 @@ def build(verbose=True):
     ckpt_o = os.path.join(objdir, "ckpt.o")
     _run([_cxx(), *common, *host_flags, "-c", os.path.join(CSRC, "ckpt.cpp"), "-o", ckpt_o])
     objs += [offload_o, ckpt_o]
-    for src in ("kernels.hip", "quant.hip"):
+    for src in ("kernels.hip", "quant.hip", "act.hip", "act_grad.hip"):
         obj = os.path.join(objdir, src.replace(".hip", ".o"))
         _run([hipcc, *common, "-x", "hip", f"--offload-arch={ARCH}",
               "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
