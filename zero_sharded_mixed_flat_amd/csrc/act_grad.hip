@@ -2,66 +2,352 @@
 // input, for MI355X (gfx950, wave64), and its C-ABI entry point.  The formulas
 // are in include/zero_flat.h.
 //
-//   weight_grad_kernel   dW = dY^T X, X restored from the checkpoint
+//   weight_grad_kernel   a tile of dW = dY^T X, X restored from the checkpoint
+//   join_kernel          adds the partial tiles of a product split over tokens
+//
+// The contraction runs over tokens, the slow axis of both operands: a matrix
+// instruction wants 8 consecutive tokens of one column per lane.  Tiles of 64
+// tokens are staged in LDS as they lie in memory ([token][column], 16 bits) and
+// read with the transposing LDS load (ds_read_b64_tr_b16: 16 lanes read 4 rows
+// of 16 columns and each lane receives one column of the 4 rows).  The codes are
+// decoded once per block on their way into LDS, between the matrix
+// instructions of the previous tile.
 
 #include "act.h"
 
 namespace zf {
 namespace {
 
-// A block does a 64 x 64 tile of dW, 16 tokens at a time, in fp32.
-constexpr int kTile = 64, kTokens = 16, kGradThreads = 256;
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef short s8v __attribute__((ext_vector_type(8)));
+typedef __bf16 b8v __attribute__((ext_vector_type(8)));
+typedef _Float16 h8v __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
 
-template <int DT, int FMT>
-__global__ __launch_bounds__(kGradThreads) void weight_grad_kernel(
-    const uint16_t* __restrict__ dy, int64_t dy_stride, const uint8_t* __restrict__ codes, int64_t pitch,
-    const float* __restrict__ scales, int blocks_per_row, int64_t rows, int64_t in_cols, int64_t out_cols,
-    int accumulate, uint16_t* dweight, uint16_t* dbias) {
-    __shared__ float a[kTokens][kTile], b[kTokens][kTile];
-    const int64_t i0 = int64_t(blockIdx.x) * kTile, o0 = int64_t(blockIdx.y) * kTile;
-    const int ti = threadIdx.x % 16, to = threadIdx.x / 16;
-    float acc[4][4] = {}, bias[4] = {};
-    for (int64_t t0 = 0; t0 < rows; t0 += kTokens) {
-        for (int e = threadIdx.x; e < kTokens * kTile; e += kGradThreads) {
-            const int r = e / kTile, c = e % kTile;
-            const int64_t t = t0 + r;
-            a[r][c] = t < rows && o0 + c < out_cols ? widen<DT>(dy[t * dy_stride + o0 + c]) : 0.0f;
-            float x = 0.0f;
-            if (t < rows && i0 + c < in_cols) {
-                float v[4];
-                decode_word<FMT>(codes[t * pitch + i0 + c], v);
-                x = widen<DT>(narrow_pair<DT>(v[0] * scales[t * blocks_per_row + (i0 + c) / kActBlock], 0.0f) & 0xffffu);
+constexpr int kTokens = 64;       // tokens per staged tile
+constexpr int kGradThreads = 256; // four waves, two by two
+
+// A block's tile: TILE outputs x TILE inputs; a wave does a quarter of it in
+// FRAGS x FRAGS 32 x 32 fragments.  LDS rows are TILE 16-bit values in segments of
+// 32 columns (64 bytes), segment s of token t kept at s ^ (t mod 4): the four rows
+// that a transposing read touches then lie in different quarters of the 256 bytes
+// that the banks span.
+template <int TILE>
+struct GradTile {
+    static constexpr int kRowBytes = 2 * TILE;
+    static constexpr int kOperandBytes = kTokens * kRowBytes;
+    static constexpr int kStageBytes = 2 * kOperandBytes;
+    static constexpr int kWave = TILE / 2;
+    static constexpr int kFrags = kWave / 32;
+    static constexpr int kOcts = TILE / kOct;                    // per row
+    static constexpr int kRowsPerPass = kGradThreads / kOcts;
+    static constexpr int kPasses = kTokens / kRowsPerPass;
+};
+
+struct GradArgs {
+    const uint16_t* dy;
+    int64_t dy_stride;
+    const uint8_t* codes;
+    int64_t pitch;
+    const float* scales;
+    int blocks_per_row;
+    int64_t rows;
+    int in_cols, out_cols;
+    int in_tiles, out_tiles;
+    int splits;
+    int64_t split_rows;  // tokens per split, a multiple of kTokens
+    int accumulate;
+    uint16_t* dweight;
+    uint16_t* dbias;
+    float* partials;       // splits > 1: [splits][out_cols][in8] fp32, then
+    float* bias_partials;  // [splits][out_cols]
+};
+
+template <int DT>
+__device__ __forceinline__ f16v mfma32(const s8v& a, const s8v& b, const f16v& c) {
+    if constexpr (DT == ZERO_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8v, a), __builtin_bit_cast(b8v, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, a), __builtin_bit_cast(h8v, b), c, 0, 0, 0);
+}
+
+// 8 tokens of one column per lane: two transposing reads, 4 tokens each.
+template <int ROW_BYTES>
+__device__ __forceinline__ s8v read_frag(const char* p) {
+    typedef __attribute__((address_space(3))) s4v* lds4;
+    const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
+    const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * ROW_BYTES));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Staged tiles t0, t0 + 64, .. of `tiles` into acc.  GUARD: columns or tokens of
+// the tile may lie outside the operands (they are staged as zero), and with
+// `bias` the column sums of dY are taken on the way.
+template <int DT, int FMT, int TILE, bool GUARD>
+__device__ __forceinline__ void grad_loop(const GradArgs& g, char* smem, int o0, int i0, int64_t t0, int tiles,
+                                          int64_t t_end, bool bias, float (&bsum)[kOct],
+                                          f16v (&acc)[GradTile<TILE>::kFrags][GradTile<TILE>::kFrags]) {
+    using G = GradTile<TILE>;
+    constexpr int F = G::kFrags, P = G::kPasses;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int oct = tid % G::kOcts, row = tid / G::kOcts;
+    // where this thread's octs go, and where its fragments start
+    const int put = row * G::kRowBytes + (((oct >> 2) ^ (row & 3)) << 6) + ((oct & 3) << 4);
+    const int l = lane & 15, grp = lane >> 4;
+    const int frag_row = (grp >> 1) * 8 + (l >> 2);
+    const int inner = ((grp & 1) * 16 + (l & 3) * 4) * 2;
+    int fa[F], fb[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+        const int sa = (wave >> 1) * F + f, sb = (wave & 1) * F + f;
+        fa[f] = frag_row * G::kRowBytes + ((sa ^ (l >> 2)) << 6) + inner;
+        fb[f] = G::kOperandBytes + frag_row * G::kRowBytes + ((sb ^ (l >> 2)) << 6) + inner;
+    }
+    const uint32_t dy_off = GUARD ? 0u : uint32_t(row * g.dy_stride + oct * kOct) * 2u;
+    const uint32_t code_off = uint32_t(row * int(g.pitch)) + oct * kOct;
+    const uint32_t scale_off = uint32_t(row * g.blocks_per_row);
+
+    u4 a[P];
+    u2 b[P];
+    float s[P];
+    const auto load = [&](int tile, int j) {
+        const int64_t t = t0 + int64_t(tile) * kTokens + j * G::kRowsPerPass;
+        if constexpr (GUARD) {
+            const int64_t tr = t + row;
+            const int o = o0 + oct * kOct, i = i0 + oct * kOct;
+            a[j] = u4{0u, 0u, 0u, 0u};
+            b[j] = u2{0u, 0u};
+            s[j] = 0.0f;
+            if (tr < t_end) {
+                if (o < g.out_cols) a[j] = load_oct_shared(g.dy + tr * g.dy_stride, o, g.out_cols);
+                if (i < g.in_cols) {
+                    b[j] = *reinterpret_cast<const u2*>(g.codes + tr * g.pitch + i);
+                    s[j] = g.scales[tr * g.blocks_per_row + i / kActBlock];
+                }
             }
-            b[r][c] = x;
+        } else {
+            const char* pa = reinterpret_cast<const char*>(g.dy + t * g.dy_stride + o0);
+            a[j] = *reinterpret_cast<const u4_any*>(pa + dy_off);
+            const uint8_t* pb = g.codes + t * g.pitch + i0;
+            b[j] = *reinterpret_cast<const u2*>(pb + code_off);
+            const float* ps = g.scales + t * g.blocks_per_row + i0 / kActBlock;
+            s[j] = ps[scale_off];
         }
-        __syncthreads();
-        for (int r = 0; r < kTokens; ++r) {
-            float x[4], y[4];
+    };
+    const auto store = [&](char* stage, int j) {
+        char* p = stage + put + j * G::kRowsPerPass * G::kRowBytes;
+        *reinterpret_cast<u4*>(p) = a[j];
+        *reinterpret_cast<u4*>(p + G::kOperandBytes) = decode_oct<DT, FMT>(b[j], s[j]);
+        if constexpr (GUARD) {
+            if (bias) {
+                float v[kOct];
+                widen_oct<DT>(a[j], v);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                y[k] = a[r][4 * to + k];
-                x[k] = b[r][4 * ti + k];
-                bias[k] += y[k];
+                for (int k = 0; k < kOct; ++k) bsum[k] += v[k];
             }
+        }
+    };
+
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < P; ++j) load(0, j);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[j][k] = __builtin_fmaf(y[j], x[k], acc[j][k]);
+    for (int j = 0; j < P; ++j) store(smem, j);
+#pragma unroll
+    for (int j = 0; j < P; ++j) load(tiles > 1 ? 1 : 0, j);
+    __syncthreads();
+    for (int it = 0; it < tiles; ++it) {
+        const char* cur = smem + (it & 1) * G::kStageBytes;
+        char* nxt = smem + ((it & 1) ^ 1) * G::kStageBytes;
+        // past the end the last tile is loaded again and never used
+        const int ahead = it + 2 < tiles ? it + 2 : tiles - 1;
+        const bool more = it + 1 < tiles;
+#pragma unroll
+        for (int ks = 0; ks < kTokens / 16; ++ks) {
+            s8v x[F], y[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f) y[f] = read_frag<G::kRowBytes>(cur + fa[f] + ks * 16 * G::kRowBytes);
+#pragma unroll
+            for (int f = 0; f < F; ++f) x[f] = read_frag<G::kRowBytes>(cur + fb[f] + ks * 16 * G::kRowBytes);
+#pragma unroll
+            for (int m = 0; m < F; ++m)
+#pragma unroll
+                for (int n = 0; n < F; ++n) acc[m][n] = mfma32<DT>(y[m], x[n], acc[m][n]);
+            constexpr int per = P / (kTokens / 16);
+#pragma unroll
+            for (int j = ks * per; j < (ks + 1) * per; ++j) {
+                if (!GUARD || more) store(nxt, j);
+                load(ahead, j);
+            }
         }
         __syncthreads();
     }
-    for (int j = 0; j < 4; ++j) {
-        const int64_t o = o0 + 4 * to + j;
-        if (o >= out_cols) continue;
-        for (int k = 0; k < 4; ++k) {
-            const int64_t i = i0 + 4 * ti + k;
-            if (i >= in_cols) continue;
-            uint16_t* out = dweight + o * in_cols + i;
-            *out = static_cast<uint16_t>(narrow<DT>(accumulate ? acc[j][k] + widen<DT>(*out) : acc[j][k]));
+}
+
+// Blocks are dispatched round-robin to the 8 XCDs; each XCD takes a contiguous
+// run of tiles, ordered so that about 32 tiles in flight form a patch of 8
+// output tiles by 4 input tiles that share operand panels in its L2.
+__device__ __forceinline__ void place_tile(int id, int count, int out_tiles, int in_tiles, int& o, int& i) {
+    constexpr int kXcds = 8, kGroup = 8;
+    const int per = count / kXcds, extra = count % kXcds;
+    const int x = id % kXcds, k = id / kXcds;
+    const int t = x * per + (x < extra ? x : extra) + k;
+    const int group = t / (kGroup * in_tiles);
+    const int first = group * kGroup;
+    const int height = out_tiles - first < kGroup ? out_tiles - first : kGroup;
+    const int r = t - first * in_tiles;
+    o = first + r % height;
+    i = r / height;
+}
+
+template <int DT, int FMT, int TILE>
+__global__ __launch_bounds__(kGradThreads) void weight_grad_kernel(GradArgs g) {
+    using G = GradTile<TILE>;
+    constexpr int F = G::kFrags;
+    __shared__ __attribute__((aligned(16))) char smem[2 * G::kStageBytes];
+    const int tiles = g.in_tiles * g.out_tiles;
+    const int split = blockIdx.x / tiles;
+    int ot, in;
+    place_tile(blockIdx.x % tiles, tiles, g.out_tiles, g.in_tiles, ot, in);
+    const int o0 = ot * TILE, i0 = in * TILE;
+    const int64_t t0 = split * g.split_rows;
+    const int64_t t_end = t0 + g.split_rows < g.rows ? t0 + g.split_rows : g.rows;
+    f16v acc[F][F];
+#pragma unroll
+    for (int m = 0; m < F; ++m)
+#pragma unroll
+        for (int n = 0; n < F; ++n) acc[m][n] = f16v{};
+    float bsum[kOct] = {};
+    const bool bias = g.dbias != nullptr && in == 0;
+    const int whole = int((t_end - t0) / kTokens);
+    const bool clean = !bias && o0 + TILE <= g.out_cols && i0 + TILE <= g.pitch && g.dy_stride < (int64_t(1) << 26) &&
+                       g.pitch < (int64_t(1) << 26);
+    const int done = clean ? whole : 0;
+    if (done > 0) grad_loop<DT, FMT, TILE, false>(g, smem, o0, i0, t0, done, t_end, false, bsum, acc);
+    const int rest = int((t_end - t0 + kTokens - 1) / kTokens) - done;
+    if (rest > 0)
+        grad_loop<DT, FMT, TILE, true>(g, smem, o0, i0, t0 + int64_t(done) * kTokens, rest, t_end, bias, bsum, acc);
+
+    // Through LDS in fp32, 32 rows of a wave's quarter at a time, into octs of a row.
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int in8 = (g.in_cols + kOct - 1) / kOct * kOct;
+    float* strip = reinterpret_cast<float*>(smem) + wave * 32 * G::kWave;
+#pragma unroll
+    for (int m = 0; m < F; ++m) {
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < F; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                strip[(8 * (r / 4) + 4 * (lane >> 5) + r % 4) * G::kWave + 32 * n + (lane & 31)] = acc[m][n][r];
+        __syncthreads();
+        constexpr int kOctsW = G::kWave / kOct, kRows = 64 / kOctsW;
+#pragma unroll
+        for (int p = 0; p < 32 / kRows; ++p) {
+            const int r = p * kRows + lane / kOctsW;
+            const int o = o0 + (wave >> 1) * G::kWave + 32 * m + r;
+            const int c = i0 + (wave & 1) * G::kWave + (lane % kOctsW) * kOct;
+            if (o >= g.out_cols || c >= g.in_cols) continue;
+            const f4* src = reinterpret_cast<const f4*>(strip + r * G::kWave + (lane % kOctsW) * kOct);
+            const f4 lo = src[0], hi = src[1];
+            if (g.splits > 1) {
+                f4* dst = reinterpret_cast<f4*>(g.partials + (int64_t(split) * g.out_cols + o) * in8 + c);
+                dst[0] = lo;
+                dst[1] = hi;
+                continue;
+            }
+            float v[kOct] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint16_t* out = g.dweight + int64_t(o) * g.in_cols;
+            if (g.accumulate) {
+                float old[kOct];
+                widen_oct<DT>(load_oct(out, c, g.in_cols), old);
+#pragma unroll
+                for (int k = 0; k < kOct; ++k) v[k] += old[k];
+            }
+            store_oct(out, c, g.in_cols, narrow_oct<DT>(v));
         }
-        if (dbias != nullptr && i0 == 0 && ti == 0)
-            dbias[o] = static_cast<uint16_t>(narrow<DT>(accumulate ? bias[j] + widen<DT>(dbias[o]) : bias[j]));
     }
+    if (!bias) return;
+    // The threads of a column's octs, added in row order.
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);
+    const int oct = tid % G::kOcts, row = tid / G::kOcts;
+#pragma unroll
+    for (int k = 0; k < kOct; ++k) sums[row * TILE + oct * kOct + k] = bsum[k];
+    __syncthreads();
+    const int o = o0 + tid;
+    if (tid >= TILE || o >= g.out_cols) return;
+    float total = sums[tid];
+    for (int r = 1; r < G::kRowsPerPass; ++r) total += sums[r * TILE + tid];
+    if (g.splits > 1) {
+        g.bias_partials[int64_t(split) * g.out_cols + o] = total;
+        return;
+    }
+    if (g.accumulate) total += widen<DT>(g.dbias[o]);
+    g.dbias[o] = static_cast<uint16_t>(narrow<DT>(total));
+}
+
+// Adds the splits' partial gradients in split order; an oct per thread.  The
+// last threads do the bias, one element each.
+constexpr int kJoinThreads = 256;
+
+template <int DT>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(GradArgs g) {
+    const int in_octs = (g.in_cols + kOct - 1) / kOct;
+    const int64_t octs = int64_t(in_octs) * g.out_cols;
+    const int64_t id = int64_t(blockIdx.x) * kJoinThreads + threadIdx.x;
+    if (id < octs) {
+        const int64_t o = id / in_octs;
+        const int c = int(id % in_octs) * kOct;
+        const float* p = g.partials + (o * in_octs + c / kOct) * kOct;
+        float v[kOct] = {};
+        for (int s = 0; s < g.splits; ++s) {
+            const f4* q = reinterpret_cast<const f4*>(p + s * octs * kOct);
+            const f4 lo = q[0], hi = q[1];
+            v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+            v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+        }
+        uint16_t* out = g.dweight + o * g.in_cols;
+        if (g.accumulate) {
+            float old[kOct];
+            widen_oct<DT>(load_oct(out, c, g.in_cols), old);
+#pragma unroll
+            for (int k = 0; k < kOct; ++k) v[k] += old[k];
+        }
+        store_oct(out, c, g.in_cols, narrow_oct<DT>(v));
+    } else if (g.dbias != nullptr && id - octs < g.out_cols) {
+        const int o = int(id - octs);
+        float total = 0.0f;
+        for (int s = 0; s < g.splits; ++s) total += g.bias_partials[int64_t(s) * g.out_cols + o];
+        if (g.accumulate) total += widen<DT>(g.dbias[o]);
+        g.dbias[o] = static_cast<uint16_t>(narrow<DT>(total));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launch glue
+// ---------------------------------------------------------------------------
+
+struct GradShape {
+    int tile, in_tiles, out_tiles, splits;
+    int64_t split_rows;
+};
+
+constexpr int kCus = 256;
+
+inline GradShape grad_shape(int64_t rows, int64_t in_cols, int64_t out_cols) {
+    const auto tiles = [&](int tile) {
+        return std::max<int64_t>(1, ceil_div(in_cols, int64_t(tile))) * ceil_div(out_cols, int64_t(tile));
+    };
+    GradShape s;
+    s.tile = tiles(256) >= kCus ? 256 : 128;
+    s.in_tiles = int(std::max<int64_t>(1, ceil_div(in_cols, int64_t(s.tile))));
+    s.out_tiles = int(ceil_div(out_cols, int64_t(s.tile)));
+    const int64_t n = tiles(s.tile), steps = std::max<int64_t>(1, ceil_div(rows, int64_t(kTokens)));
+    // few tiles and many tokens: enough splits for two blocks per CU, of at least 8 staged tiles each
+    int64_t want = n >= kCus ? 1 : std::min(ceil_div(2 * kCus, n), std::max<int64_t>(1, steps / 8));
+    s.split_rows = ceil_div(steps, want) * kTokens;
+    s.splits = int(std::max<int64_t>(1, ceil_div(rows, s.split_rows)));
+    return s;
 }
 
 inline bool weight_grad_sizes_ok(int64_t rows, int64_t in_cols, int64_t out_cols) {
@@ -69,7 +355,15 @@ inline bool weight_grad_sizes_ok(int64_t rows, int64_t in_cols, int64_t out_cols
            (in_cols == 0 || out_cols <= ZERO_MAX_ELEMS / in_cols);
 }
 
-inline int64_t weight_grad_workspace(int64_t rows, int64_t in_cols, int64_t out_cols) { return 0; }
+inline int64_t partial_floats(const GradShape& s, int64_t in_cols, int64_t out_cols) {
+    return s.splits > 1 ? int64_t(s.splits) * out_cols * ceil_div(in_cols, int64_t(kOct)) * kOct : 0;
+}
+
+inline int64_t weight_grad_workspace(int64_t rows, int64_t in_cols, int64_t out_cols) {
+    if (rows == 0 || out_cols == 0) return 0;
+    const GradShape s = grad_shape(rows, in_cols, out_cols);
+    return s.splits > 1 ? 4 * (partial_floats(s, in_cols, out_cols) + s.splits * out_cols) : 0;
+}
 
 }  // namespace
 }  // namespace zf
@@ -113,14 +407,24 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const voi
                           flat("dbias", dbias, 2 * out_cols, true),
                           flat("workspace", workspace, wb, true)};
     if (int rc = check_overlaps(fn, areas, 6)) return rc;
-    if (rows == 0 && accumulate) return ok();
+    if ((rows == 0 && accumulate) || (in_cols == 0 && dbias == nullptr)) return ok();
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid(unsigned(std::max<int64_t>(1, ceil_div(in_cols, int64_t(kTile)))),
-                    unsigned(ceil_div(out_cols, int64_t(kTile))));
-    const hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
-        return launch(weight_grad_kernel<decltype(dt)::value, decltype(fmt)::value>, grid, dim3(kGradThreads), s,
-                      in16(dy), dy_stride, in8(codes), pitch, scales, int(bpr), rows, in_cols, out_cols, accumulate,
-                      out16(dweight), out16(dbias));
+    const GradShape sh = grad_shape(rows, in_cols, out_cols);
+    float* partials = static_cast<float*>(workspace);
+    const GradArgs args{in16(dy), dy_stride, in8(codes), pitch, scales, int(bpr), rows, int(in_cols), int(out_cols),
+                        sh.in_tiles, sh.out_tiles, sh.splits, sh.split_rows, accumulate, out16(dweight), out16(dbias),
+                        partials, sh.splits > 1 ? partials + partial_floats(sh, in_cols, out_cols) : nullptr};
+    const dim3 grid(unsigned(int64_t(sh.in_tiles) * sh.out_tiles * sh.splits));
+    hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
+        constexpr int D = decltype(dt)::value, M = decltype(fmt)::value;
+        return sh.tile == 256 ? launch(weight_grad_kernel<D, M, 256>, grid, dim3(kGradThreads), s, args)
+                              : launch(weight_grad_kernel<D, M, 128>, grid, dim3(kGradThreads), s, args);
+    });
+    if (e != hipSuccess || sh.splits <= 1) return hip_status(e, fn);
+    const int64_t threads = ceil_div(in_cols, int64_t(kOct)) * out_cols + (dbias != nullptr ? out_cols : 0);
+    e = with_dtype(dtype, [&](auto dt) {
+        return launch(join_kernel<decltype(dt)::value>, dim3(unsigned(ceil_div(threads, int64_t(kJoinThreads)))),
+                      dim3(kJoinThreads), s, args);
     });
     return hip_status(e, fn);
 }
