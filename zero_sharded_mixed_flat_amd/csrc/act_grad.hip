@@ -63,6 +63,21 @@ struct GradArgs {
     float* bias_partials;  // [splits][out_cols]
 };
 
+// Order of a 16-token step's instructions: after each matrix instruction, which
+// keeps the matrix unit busy for 8 issue slots, one LDS read and a few of the
+// others, so that a lone wave per SIMD never leaves it idle.
+template <bool BIAS>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);          // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x002, BIAS ? 6 : 4, 0);  // VALU
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);          // LDS write
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);          // global load
+    }
+}
+
 template <int DT>
 __device__ __forceinline__ f16v mfma32(const s8v& a, const s8v& b, const f16v& c) {
     if constexpr (DT == ZERO_BF16)
@@ -80,15 +95,24 @@ __device__ __forceinline__ s8v read_frag(const char* p) {
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Staged tiles t0, t0 + 64, .. of `tiles` into acc.  GUARD: columns or tokens of
-// the tile may lie outside the operands (they are staged as zero), and with
-// `bias` the column sums of dY are taken on the way.
-template <int DT, int FMT, int TILE, bool GUARD>
+// How a run of staged tiles is loaded.  kWhole: every token and column of it
+// lies in the operands.  kGuarded: some may lie outside and are staged as zero.
+enum { kWhole, kGuarded };
+
+// Staged tiles t0, t0 + 64, .. of `tiles` into acc and, with BIAS, the column
+// sums of dY.  While tile k is multiplied, tile k + 1 goes from registers to the
+// other LDS stage and tile k + 2 is loaded into the registers this frees, so a
+// load has a whole tile's time (2048 cycles of matrix instructions at 256 x 256) to
+// arrive.  The fragments of 16 tokens are read while the previous 16 are
+// multiplied; the barrier stands before the last 16 of a tile, whose fragments
+// are in registers by then, so that the next tile's first ones can be read under
+// their multiplication.
+template <int DT, int FMT, int TILE, int MODE, bool BIAS>
 __device__ __forceinline__ void grad_loop(const GradArgs& g, char* smem, int o0, int i0, int64_t t0, int tiles,
-                                          int64_t t_end, bool bias, float (&bsum)[kOct],
+                                          int64_t t_end, float (&bsum)[kOct],
                                           f16v (&acc)[GradTile<TILE>::kFrags][GradTile<TILE>::kFrags]) {
     using G = GradTile<TILE>;
-    constexpr int F = G::kFrags, P = G::kPasses;
+    constexpr int F = G::kFrags, P = G::kPasses, kSteps = kTokens / 16;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int oct = tid % G::kOcts, row = tid / G::kOcts;
     // where this thread's octs go, and where its fragments start
@@ -103,84 +127,111 @@ __device__ __forceinline__ void grad_loop(const GradArgs& g, char* smem, int o0,
         fa[f] = frag_row * G::kRowBytes + ((sa ^ (l >> 2)) << 6) + inner;
         fb[f] = G::kOperandBytes + frag_row * G::kRowBytes + ((sb ^ (l >> 2)) << 6) + inner;
     }
-    const uint32_t dy_off = GUARD ? 0u : uint32_t(row * g.dy_stride + oct * kOct) * 2u;
-    const uint32_t code_off = uint32_t(row * int(g.pitch)) + oct * kOct;
-    const uint32_t scale_off = uint32_t(row * g.blocks_per_row);
 
     u4 a[P];
     u2 b[P];
     float s[P];
+    // kWhole: one uniform base per operand and a constant 32-bit offset per pass
+    uint32_t oa[P], ob[P], os[P];
+    const char* pa = reinterpret_cast<const char*>(g.dy + t0 * g.dy_stride + o0);
+    const char* pb = reinterpret_cast<const char*>(g.codes + t0 * g.pitch + i0);
+    const char* ps = reinterpret_cast<const char*>(g.scales + t0 * g.blocks_per_row + i0 / kActBlock);
+    if constexpr (MODE == kWhole) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const uint32_t r = uint32_t(row + j * G::kRowsPerPass);
+            oa[j] = (r * uint32_t(g.dy_stride) + oct * kOct) * 2u;
+            ob[j] = r * uint32_t(g.pitch) + oct * kOct;
+            os[j] = r * uint32_t(g.blocks_per_row) * 4u;
+        }
+    }
     const auto load = [&](int tile, int j) {
-        const int64_t t = t0 + int64_t(tile) * kTokens + j * G::kRowsPerPass;
-        if constexpr (GUARD) {
-            const int64_t tr = t + row;
+        if constexpr (MODE == kGuarded) {
+            const int64_t t = t0 + int64_t(tile) * kTokens + j * G::kRowsPerPass + row;
             const int o = o0 + oct * kOct, i = i0 + oct * kOct;
             a[j] = u4{0u, 0u, 0u, 0u};
             b[j] = u2{0u, 0u};
             s[j] = 0.0f;
-            if (tr < t_end) {
-                if (o < g.out_cols) a[j] = load_oct_shared(g.dy + tr * g.dy_stride, o, g.out_cols);
+            if (t < t_end) {
+                if (o < g.out_cols) a[j] = load_oct_shared(g.dy + t * g.dy_stride, o, g.out_cols);
                 if (i < g.in_cols) {
-                    b[j] = *reinterpret_cast<const u2*>(g.codes + tr * g.pitch + i);
-                    s[j] = g.scales[tr * g.blocks_per_row + i / kActBlock];
+                    b[j] = *reinterpret_cast<const u2*>(g.codes + t * g.pitch + i);
+                    s[j] = g.scales[t * g.blocks_per_row + i / kActBlock];
                 }
             }
         } else {
-            const char* pa = reinterpret_cast<const char*>(g.dy + t * g.dy_stride + o0);
-            a[j] = *reinterpret_cast<const u4_any*>(pa + dy_off);
-            const uint8_t* pb = g.codes + t * g.pitch + i0;
-            b[j] = *reinterpret_cast<const u2*>(pb + code_off);
-            const float* ps = g.scales + t * g.blocks_per_row + i0 / kActBlock;
-            s[j] = ps[scale_off];
+            a[j] = *reinterpret_cast<const u4_any*>(pa + oa[j]);
+            b[j] = *reinterpret_cast<const u2*>(pb + ob[j]);
+            s[j] = *reinterpret_cast<const float*>(ps + os[j]);
         }
+    };
+    const auto advance = [&](bool more) {
+        pa += more ? 2 * kTokens * g.dy_stride : 0;
+        pb += more ? kTokens * g.pitch : 0;
+        ps += more ? int64_t(4) * kTokens * g.blocks_per_row : 0;
     };
     const auto store = [&](char* stage, int j) {
         char* p = stage + put + j * G::kRowsPerPass * G::kRowBytes;
         *reinterpret_cast<u4*>(p) = a[j];
         *reinterpret_cast<u4*>(p + G::kOperandBytes) = decode_oct<DT, FMT>(b[j], s[j]);
-        if constexpr (GUARD) {
-            if (bias) {
-                float v[kOct];
-                widen_oct<DT>(a[j], v);
+    };
+    // `keep` is all ones, or 0 for a tile that is only staged again
+    const auto sum = [&](int j, uint32_t keep) {
+        if constexpr (BIAS) {
+            float v[kOct];
+            widen_oct<DT>(a[j] & keep, v);
 #pragma unroll
-                for (int k = 0; k < kOct; ++k) bsum[k] += v[k];
-            }
+            for (int k = 0; k < kOct; ++k) bsum[k] += v[k];
         }
+    };
+    s8v x[2][F], y[2][F];
+    const auto read = [&](const char* stage, int ks, int set) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) y[set][f] = read_frag<G::kRowBytes>(stage + fa[f] + ks * 16 * G::kRowBytes);
+#pragma unroll
+        for (int f = 0; f < F; ++f) x[set][f] = read_frag<G::kRowBytes>(stage + fb[f] + ks * 16 * G::kRowBytes);
     };
 
 #pragma unroll
     for (int j = 0; j < P; ++j) load(0, j);
+    advance(tiles > 1);
 #pragma unroll
-    for (int j = 0; j < P; ++j) store(smem, j);
-#pragma unroll
-    for (int j = 0; j < P; ++j) load(tiles > 1 ? 1 : 0, j);
+    for (int j = 0; j < P; ++j) {
+        store(smem, j);
+        sum(j, ~0u);
+        load(tiles > 1 ? 1 : 0, j);
+    }
     __syncthreads();
+    read(smem, 0, 0);
     for (int it = 0; it < tiles; ++it) {
         const char* cur = smem + (it & 1) * G::kStageBytes;
         char* nxt = smem + ((it & 1) ^ 1) * G::kStageBytes;
-        // past the end the last tile is loaded again and never used
+        // past the end the last tile is staged again and never used
+        advance(it + 2 < tiles);
         const int ahead = it + 2 < tiles ? it + 2 : tiles - 1;
-        const bool more = it + 1 < tiles;
+        const uint32_t keep = it + 1 < tiles ? ~0u : 0u;
 #pragma unroll
-        for (int ks = 0; ks < kTokens / 16; ++ks) {
-            s8v x[F], y[F];
-#pragma unroll
-            for (int f = 0; f < F; ++f) y[f] = read_frag<G::kRowBytes>(cur + fa[f] + ks * 16 * G::kRowBytes);
-#pragma unroll
-            for (int f = 0; f < F; ++f) x[f] = read_frag<G::kRowBytes>(cur + fb[f] + ks * 16 * G::kRowBytes);
+        for (int ks = 0; ks < kSteps; ++ks) {
+            if (ks == kSteps - 1) __syncthreads();
+            read(ks == kSteps - 1 ? nxt : cur, (ks + 1) % kSteps, (ks + 1) & 1);
 #pragma unroll
             for (int m = 0; m < F; ++m)
 #pragma unroll
-                for (int n = 0; n < F; ++n) acc[m][n] = mfma32<DT>(y[m], x[n], acc[m][n]);
-            constexpr int per = P / (kTokens / 16);
+                for (int n = 0; n < F; ++n) acc[m][n] = mfma32<DT>(y[ks & 1][m], x[ks & 1][n], acc[m][n]);
+            // the passes are spread over all but the last 16 tokens
+            if (ks < kSteps - 1) {
 #pragma unroll
-            for (int j = ks * per; j < (ks + 1) * per; ++j) {
-                if (!GUARD || more) store(nxt, j);
-                load(ahead, j);
+                for (int j = ks * P / (kSteps - 1); j < (ks + 1) * P / (kSteps - 1); ++j) {
+                    store(nxt, j);
+                    sum(j, keep);
+                    load(ahead, j);
+                }
             }
+            if constexpr (MODE == kWhole && TILE == 256) interleave<BIAS>();
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __syncthreads();
     }
+    __syncthreads();
 }
 
 // Blocks are dispatched round-robin to the 8 XCDs; each XCD takes a contiguous
@@ -218,14 +269,21 @@ __global__ __launch_bounds__(kGradThreads) void weight_grad_kernel(GradArgs g) {
         for (int n = 0; n < F; ++n) acc[m][n] = f16v{};
     float bsum[kOct] = {};
     const bool bias = g.dbias != nullptr && in == 0;
-    const int whole = int((t_end - t0) / kTokens);
-    const bool clean = !bias && o0 + TILE <= g.out_cols && i0 + TILE <= g.pitch && g.dy_stride < (int64_t(1) << 26) &&
-                       g.pitch < (int64_t(1) << 26);
-    const int done = clean ? whole : 0;
-    if (done > 0) grad_loop<DT, FMT, TILE, false>(g, smem, o0, i0, t0, done, t_end, false, bsum, acc);
-    const int rest = int((t_end - t0 + kTokens - 1) / kTokens) - done;
-    if (rest > 0)
-        grad_loop<DT, FMT, TILE, true>(g, smem, o0, i0, t0 + int64_t(done) * kTokens, rest, t_end, bias, bsum, acc);
+    // Tiles that lie inside the operands take the unguarded loads, with 32-bit
+    // offsets within 64 tokens; the last tokens and the edges the guarded ones.
+    const bool inside = o0 + TILE <= g.out_cols && i0 + TILE <= g.pitch && g.dy_stride < (int64_t(1) << 24) &&
+                        g.pitch < (int64_t(1) << 24);
+    const int all = int((t_end - t0 + kTokens - 1) / kTokens);
+    const int whole = inside ? int((t_end - t0) / kTokens) : 0;
+    if (whole > 0) {
+        if (bias)
+            grad_loop<DT, FMT, TILE, kWhole, true>(g, smem, o0, i0, t0, whole, t_end, bsum, acc);
+        else
+            grad_loop<DT, FMT, TILE, kWhole, false>(g, smem, o0, i0, t0, whole, t_end, bsum, acc);
+    }
+    if (all > whole)
+        grad_loop<DT, FMT, TILE, kGuarded, true>(g, smem, o0, i0, t0 + int64_t(whole) * kTokens, all - whole, t_end, bsum,
+                                                 acc);
 
     // Through LDS in fp32, 32 rows of a wave's quarter at a time, into octs of a row.
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
