@@ -124,11 +124,12 @@ def test_no_rows_no_columns(abi):
         torch.cuda.synchronize()
         assert (m.bits() == want).all() and (b.bits() == want).all()
     # no input columns: only the bias gradient is left
-    dy = Mat(9, 5, "bf16", np.full((9, 5), 0x3F80, np.uint16))
-    ws = torch.empty(max(abi.zero_act_weight_grad_workspace_bytes(9, 0, 5), 16), dtype=torch.uint8, device="cuda")
-    abi.zero_act_weight_grad(dy.t, 5, "bf16", 0, 0, 1, 9, 0, 5, False, 0, b.view.view(-1), ws)
-    torch.cuda.synchronize()
-    assert (wide(b.bits(), "bf16") == 9).all()
+    for rows in (9, 256):
+        dy = Mat(rows, 5, "bf16", np.full((rows, 5), 0x3F80, np.uint16))
+        ws = torch.empty(max(abi.zero_act_weight_grad_workspace_bytes(rows, 0, 5), 16), dtype=torch.uint8, device="cuda")
+        abi.zero_act_weight_grad(dy.t, 5, "bf16", 0, 0, 1, rows, 0, 5, False, 0, b.view.view(-1), ws)
+        torch.cuda.synchronize()
+        assert (wide(b.bits(), "bf16") == rows).all()
     abi.zero_act_weight_grad(0, 0, "bf16", 0, 0, 1, 9, 7, 0, False, 0, None, None, workspace_bytes=0)
 
 

@@ -6,7 +6,7 @@
 //   join_kernel          adds the partial tiles of a product split over tokens
 //
 // The contraction runs over tokens, the slow axis of both operands: a matrix
-// instruction wants 8 consecutive tokens of one column per lane.  Tiles of 64
+// instruction wants 8 consecutive tokens of one column per lane.  Tiles of 32
 // tokens are staged in LDS as they lie in memory ([token][column], 16 bits) and
 // read with the transposing LDS load (ds_read_b64_tr_b16: 16 lanes read 4 rows
 // of 16 columns and each lane receives one column of the 4 rows).  The codes are
@@ -22,33 +22,38 @@ typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));
 typedef __bf16 b8v __attribute__((ext_vector_type(8)));
 typedef _Float16 h8v __attribute__((ext_vector_type(8)));
-typedef float f16v __attribute__((ext_vector_type(16)));
 
-constexpr int kTokens = 64;       // tokens per staged tile
+constexpr int kTokens = 32;       // tokens per staged tile: one matrix instruction's depth
 constexpr int kGradThreads = 256; // four waves, two by two
 
 // A block's tile: TILE outputs x TILE inputs; a wave does a quarter of it in
-// FRAGS x FRAGS 32 x 32 fragments.  LDS rows are TILE 16-bit values in segments of
-// 32 columns (64 bytes), segment s of token t kept at s ^ (t mod 4): the four rows
-// that a transposing read touches then lie in different quarters of the 256 bytes
-// that the banks span.
+// FRAGS x FRAGS 16 x 16 fragments (the 16 x 16 x 32 instruction: 2040 TFLOP/s
+// sustained on random operands held in registers, where 32 x 32 x 16 reaches 1785,
+// as the clock falls with the power drawn).  LDS rows are TILE 16-bit values in units
+// of 16 columns (32 bytes); token t's units are kept at unit ^ x(t), x(t) = t mod 4
+// + 4 (t / 8 mod 2), so that the 16 rows which a transposing read touches spread
+// evenly over the banks.
 template <int TILE>
 struct GradTile {
     static constexpr int kRowBytes = 2 * TILE;
     static constexpr int kOperandBytes = kTokens * kRowBytes;
     static constexpr int kStageBytes = 2 * kOperandBytes;
     static constexpr int kWave = TILE / 2;
-    static constexpr int kFrags = kWave / 32;
+    static constexpr int kFrags = kWave / 16;
     static constexpr int kOcts = TILE / kOct;                    // per row
     static constexpr int kRowsPerPass = kGradThreads / kOcts;
     static constexpr int kPasses = kTokens / kRowsPerPass;
 };
 
+// The input operand: codes (FMT a ZERO_ACT_* format, decoded while staged) or, for
+// kDecoded, 16-bit values that a pass over the checkpoint restored beforehand.
+constexpr int kDecoded = 0;
+
 struct GradArgs {
     const uint16_t* dy;
     int64_t dy_stride;
-    const uint8_t* codes;
-    int64_t pitch;
+    const uint8_t* input;
+    int64_t pitch;  // bytes from row to row of the input
     const float* scales;
     int blocks_per_row;
     int64_t rows;
@@ -63,27 +68,27 @@ struct GradArgs {
     float* bias_partials;  // [splits][out_cols]
 };
 
-// Order of a 16-token step's instructions: after each matrix instruction, which
-// keeps the matrix unit busy for 8 issue slots, one LDS read and a few of the
-// others, so that a lone wave per SIMD never leaves it idle.
-template <bool BIAS>
+// Order of a tile's instructions: after every two matrix instructions, which keep
+// the matrix unit busy for 8 issue slots, one LDS read and a few of the others, so
+// that a lone wave per SIMD does not leave it idle.
+template <int F, int VALU>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // MFMA
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);          // LDS read
-        __builtin_amdgcn_sched_group_barrier(0x002, BIAS ? 6 : 4, 0);  // VALU
-        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);          // LDS write
-        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);          // global load
+    for (int i = 0; i < F * F / 2; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);             // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);             // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);          // VALU
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);             // LDS write
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);             // global load
     }
 }
 
 template <int DT>
-__device__ __forceinline__ f16v mfma32(const s8v& a, const s8v& b, const f16v& c) {
+__device__ __forceinline__ f4 mfma16(const s8v& a, const s8v& b, const f4& c) {
     if constexpr (DT == ZERO_BF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8v, a), __builtin_bit_cast(b8v, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8v, a), __builtin_bit_cast(b8v, b), c, 0, 0, 0);
     else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, a), __builtin_bit_cast(h8v, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, a), __builtin_bit_cast(h8v, b), c, 0, 0, 0);
 }
 
 // 8 tokens of one column per lane: two transposing reads, 4 tokens each.
@@ -95,150 +100,227 @@ __device__ __forceinline__ s8v read_frag(const char* p) {
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// How a run of staged tiles is loaded.  kWhole: every token and column of it
-// lies in the operands.  kGuarded: some may lie outside and are staged as zero.
+__device__ __forceinline__ constexpr int swizzle(int token) { return (token & 3) | ((token >> 1) & 4); }
+
+// How a block's tokens are loaded.  kGuarded: every load is checked against the
+// operands' edges, and what lies outside is staged as zero.  kWhole, for at least
+// 128 tokens: only the last 64 tokens, which are staged first, are checked.  The
+// other loads need no check: an oct that lies outside the columns reads the row's
+// first columns instead and one that straddles the end of a row reads on into the
+// next row (these columns of the product are not stored), and the rows exist.
 enum { kWhole, kGuarded };
 
-// Staged tiles t0, t0 + 64, .. of `tiles` into acc and, with BIAS, the column
-// sums of dY.  While tile k is multiplied, tile k + 1 goes from registers to the
-// other LDS stage and tile k + 2 is loaded into the registers this frees, so a
-// load has a whole tile's time (2048 cycles of matrix instructions at 256 x 256) to
-// arrive.  The fragments of 16 tokens are read while the previous 16 are
-// multiplied; the barrier stands before the last 16 of a tile, whose fragments
-// are in registers by then, so that the next tile's first ones can be read under
-// their multiplication.
+// One tile of dW over tokens [t0, t_end), BIAS: with the column sums of dY.
+//
+// Tokens are staged 32 at a time, in pairs of such steps; the last pair comes
+// first.  While step k is multiplied from registers, the fragments of step k + 1
+// are read from one LDS stage, step k + 2 goes from registers to the other (whose
+// step k every wave has read before the barrier at the start), and step k + 4 is
+// loaded into the registers this frees: two steps' time for a load to arrive, and
+// one barrier per step.
 template <int DT, int FMT, int TILE, int MODE, bool BIAS>
-__device__ __forceinline__ void grad_loop(const GradArgs& g, char* smem, int o0, int i0, int64_t t0, int tiles,
-                                          int64_t t_end, float (&bsum)[kOct],
-                                          f16v (&acc)[GradTile<TILE>::kFrags][GradTile<TILE>::kFrags]) {
+__device__ __forceinline__ void grad_tile(const GradArgs& g, char* smem, int o0, int i0, int64_t t0, int64_t t_end,
+                                          int split) {
     using G = GradTile<TILE>;
-    constexpr int F = G::kFrags, P = G::kPasses, kSteps = kTokens / 16;
+    constexpr int F = G::kFrags, P = G::kPasses;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int oct = tid % G::kOcts, row = tid / G::kOcts;
-    // where this thread's octs go, and where its fragments start
-    const int put = row * G::kRowBytes + (((oct >> 2) ^ (row & 3)) << 6) + ((oct & 3) << 4);
     const int l = lane & 15, grp = lane >> 4;
-    const int frag_row = (grp >> 1) * 8 + (l >> 2);
-    const int inner = ((grp & 1) * 16 + (l & 3) * 4) * 2;
+    // first of this lane's rows in a fragment, and its 4 columns there
+    const int frag = (grp * 8 + (l >> 2)) * G::kRowBytes + (l & 3) * 8;
+    const int frag_x = swizzle(grp * 8 + (l >> 2));
     int fa[F], fb[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-        const int sa = (wave >> 1) * F + f, sb = (wave & 1) * F + f;
-        fa[f] = frag_row * G::kRowBytes + ((sa ^ (l >> 2)) << 6) + inner;
-        fb[f] = G::kOperandBytes + frag_row * G::kRowBytes + ((sb ^ (l >> 2)) << 6) + inner;
+        fa[f] = frag + ((((wave >> 1) * F + f) ^ frag_x) << 5);
+        fb[f] = frag + ((((wave & 1) * F + f) ^ frag_x) << 5) + G::kOperandBytes;
     }
+    // at least one pair: without tokens it is staged as zeros
+    const int pairs = int((t_end - t0 + 2 * kTokens - 1) / (2 * kTokens));
+    const int steps = 2 * (pairs > 0 ? pairs : 1);
 
-    u4 a[P];
-    u2 b[P];
-    float s[P];
-    // kWhole: one uniform base per operand and a constant 32-bit offset per pass
-    uint32_t oa[P], ob[P], os[P];
-    const char* pa = reinterpret_cast<const char*>(g.dy + t0 * g.dy_stride + o0);
-    const char* pb = reinterpret_cast<const char*>(g.codes + t0 * g.pitch + i0);
-    const char* ps = reinterpret_cast<const char*>(g.scales + t0 * g.blocks_per_row + i0 / kActBlock);
-    if constexpr (MODE == kWhole) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const uint32_t r = uint32_t(row + j * G::kRowsPerPass);
-            oa[j] = (r * uint32_t(g.dy_stride) + oct * kOct) * 2u;
-            ob[j] = r * uint32_t(g.pitch) + oct * kOct;
-            os[j] = r * uint32_t(g.blocks_per_row) * 4u;
-        }
-    }
-    const auto load = [&](int tile, int j) {
-        if constexpr (MODE == kGuarded) {
-            const int64_t t = t0 + int64_t(tile) * kTokens + j * G::kRowsPerPass + row;
-            const int o = o0 + oct * kOct, i = i0 + oct * kOct;
-            a[j] = u4{0u, 0u, 0u, 0u};
-            b[j] = u2{0u, 0u};
-            s[j] = 0.0f;
-            if (t < t_end) {
-                if (o < g.out_cols) a[j] = load_oct_shared(g.dy + t * g.dy_stride, o, g.out_cols);
-                if (i < g.in_cols) {
-                    b[j] = *reinterpret_cast<const u2*>(g.codes + t * g.pitch + i);
-                    s[j] = g.scales[t * g.blocks_per_row + i / kActBlock];
-                }
+    constexpr int kBytes = FMT == kDecoded ? 2 : 1;  // per input element
+    typedef std::conditional_t<FMT == kDecoded, u4, u2> InputOct;
+    u4 a[2][P];
+    InputOct b[2][P];
+    float s[2][P];
+    const int o = o0 + oct * kOct, i = i0 + oct * kOct;
+    const auto load_checked = [&](int step, int set, int j) {
+        const int64_t t = t0 + int64_t(step) * kTokens + j * G::kRowsPerPass + row;
+        a[set][j] = u4{0u, 0u, 0u, 0u};
+        b[set][j] = InputOct{};
+        s[set][j] = 0.0f;
+        if (t < t_end) {
+            if (o < g.out_cols) a[set][j] = load_oct_shared(g.dy + t * g.dy_stride, o, g.out_cols);
+            if (i < g.in_cols) {
+                b[set][j] = *reinterpret_cast<const InputOct*>(g.input + t * g.pitch + i * kBytes);
+                if constexpr (FMT != kDecoded) s[set][j] = g.scales[t * g.blocks_per_row + i / kActBlock];
             }
-        } else {
-            a[j] = *reinterpret_cast<const u4_any*>(pa + oa[j]);
-            b[j] = *reinterpret_cast<const u2*>(pb + ob[j]);
-            s[j] = *reinterpret_cast<const float*>(ps + os[j]);
         }
     };
-    const auto advance = [&](bool more) {
+    // kWhole: a uniform base per operand and pass, and constant 32-bit offsets
+    const char* pa = reinterpret_cast<const char*>(g.dy + t0 * g.dy_stride);
+    const char* pb = reinterpret_cast<const char*>(g.input + t0 * g.pitch);
+    const char* ps = reinterpret_cast<const char*>(g.scales + t0 * g.blocks_per_row + i0 / kActBlock);
+    const uint32_t oa = (uint32_t(row) * uint32_t(g.dy_stride) + (o < g.out_cols ? o : 0)) * 2u;
+    const uint32_t ob = uint32_t(row) * uint32_t(g.pitch) + (i < g.in_cols ? i : 0) * kBytes;
+    const uint32_t os = uint32_t(row) * uint32_t(g.blocks_per_row) * 4u;
+    int loaded = 0;
+    // the next step's pass j into `set`; `last`: then on to the step after it, or past
+    // the end the last one again (staged but never used)
+    const auto load = [&](int set, int j) {
+        if constexpr (MODE == kGuarded) {
+            load_checked(loaded, set, j);
+        } else {
+            constexpr int64_t rp = G::kRowsPerPass;
+            a[set][j] = *reinterpret_cast<const u4_any*>(pa + 2 * j * rp * g.dy_stride + oa);
+            b[set][j] = *reinterpret_cast<const InputOct*>(pb + j * rp * g.pitch + ob);
+            if constexpr (FMT != kDecoded) s[set][j] = *reinterpret_cast<const float*>(ps + 4 * j * rp * g.blocks_per_row + os);
+        }
+    };
+    const auto advance = [&]() {
+        ++loaded;
+        const bool more = loaded < steps - 2;
         pa += more ? 2 * kTokens * g.dy_stride : 0;
         pb += more ? kTokens * g.pitch : 0;
         ps += more ? int64_t(4) * kTokens * g.blocks_per_row : 0;
     };
-    const auto store = [&](char* stage, int j) {
-        char* p = stage + put + j * G::kRowsPerPass * G::kRowBytes;
-        *reinterpret_cast<u4*>(p) = a[j];
-        *reinterpret_cast<u4*>(p + G::kOperandBytes) = decode_oct<DT, FMT>(b[j], s[j]);
-    };
-    // `keep` is all ones, or 0 for a tile that is only staged again
-    const auto sum = [&](int j, uint32_t keep) {
+    float bsum[kOct] = {};
+    const auto store = [&](int set, int j, bool fresh) {
+        const int r = row + j * G::kRowsPerPass;
+        char* p = smem + set * G::kStageBytes + r * G::kRowBytes + (((oct >> 1) ^ swizzle(r)) << 5) + ((oct & 1) << 4);
+        *reinterpret_cast<u4*>(p) = a[set][j];
+        if constexpr (FMT == kDecoded)
+            *reinterpret_cast<u4*>(p + G::kOperandBytes) = b[set][j];
+        else
+            *reinterpret_cast<u4*>(p + G::kOperandBytes) = decode_oct<DT, FMT>(b[set][j], s[set][j]);
         if constexpr (BIAS) {
             float v[kOct];
-            widen_oct<DT>(a[j] & keep, v);
+            widen_oct<DT>(a[set][j] & (fresh ? ~0u : 0u), v);
 #pragma unroll
             for (int k = 0; k < kOct; ++k) bsum[k] += v[k];
         }
     };
-    s8v x[2][F], y[2][F];
-    const auto read = [&](const char* stage, int ks, int set) {
-#pragma unroll
-        for (int f = 0; f < F; ++f) y[set][f] = read_frag<G::kRowBytes>(stage + fa[f] + ks * 16 * G::kRowBytes);
-#pragma unroll
-        for (int f = 0; f < F; ++f) x[set][f] = read_frag<G::kRowBytes>(stage + fb[f] + ks * 16 * G::kRowBytes);
-    };
 
+    s8v y[2][F], x[F];  // outputs' and inputs' fragments
 #pragma unroll
-    for (int j = 0; j < P; ++j) load(0, j);
-    advance(tiles > 1);
+    for (int set = 0; set < 2; ++set)
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        store(smem, j);
-        sum(j, ~0u);
-        load(tiles > 1 ? 1 : 0, j);
+        for (int j = 0; j < P; ++j) load_checked(steps - 2 + set, set, j);
+#pragma unroll
+    for (int set = 0; set < 2; ++set) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            store(set, j, true);
+            load(set, j);
+        }
+        advance();
+        // the loop's waits assume the loads in this order
+        __builtin_amdgcn_sched_barrier(0);
     }
+    f4 acc[F][F];
+#pragma unroll
+    for (int m = 0; m < F; ++m)
+#pragma unroll
+        for (int n = 0; n < F; ++n) {
+            // The empty asm makes each zero a value of its own: accumulators that start from one
+            // shared constant were moved between registers in every pass of the loop.
+            acc[m][n] = f4{};
+            asm("" : "+a"(acc[m][n]));
+        }
     __syncthreads();
-    read(smem, 0, 0);
-    for (int it = 0; it < tiles; ++it) {
-        const char* cur = smem + (it & 1) * G::kStageBytes;
-        char* nxt = smem + ((it & 1) ^ 1) * G::kStageBytes;
-        // past the end the last tile is staged again and never used
-        advance(it + 2 < tiles);
-        const int ahead = it + 2 < tiles ? it + 2 : tiles - 1;
-        const uint32_t keep = it + 1 < tiles ? ~0u : 0u;
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-            if (ks == kSteps - 1) __syncthreads();
-            read(ks == kSteps - 1 ? nxt : cur, (ks + 1) % kSteps, (ks + 1) & 1);
+    for (int f = 0; f < F; ++f) {
+        y[0][f] = read_frag<G::kRowBytes>(smem + fa[f]);
+        x[f] = read_frag<G::kRowBytes>(smem + fb[f]);
+    }
+    const auto step = [&](int k, auto parity) {
+        constexpr int S = decltype(parity)::value;
+        const char* next = smem + (S ^ 1) * G::kStageBytes;
+        __syncthreads();
 #pragma unroll
-            for (int m = 0; m < F; ++m)
+        for (int n = 0; n < F; ++n) {
+            y[S ^ 1][n] = read_frag<G::kRowBytes>(next + fa[n]);
 #pragma unroll
-                for (int n = 0; n < F; ++n) acc[m][n] = mfma32<DT>(y[ks & 1][m], x[ks & 1][n], acc[m][n]);
-            // the passes are spread over all but the last 16 tokens
-            if (ks < kSteps - 1) {
-#pragma unroll
-                for (int j = ks * P / (kSteps - 1); j < (ks + 1) * P / (kSteps - 1); ++j) {
-                    store(nxt, j);
-                    sum(j, keep);
-                    load(ahead, j);
-                }
+            for (int m = 0; m < F; ++m) acc[m][n] = mfma16<DT>(y[S][m], x[n], acc[m][n]);
+            x[n] = read_frag<G::kRowBytes>(next + fb[n]);
+            constexpr int every = F / P;
+            if (n % every == every - 1) {
+                store(S, n / every, k + 2 < steps);
+                load(S, n / every);
             }
-            if constexpr (MODE == kWhole && TILE == 256) interleave<BIAS>();
-            __builtin_amdgcn_sched_barrier(0);
+        }
+        advance();
+        if constexpr (MODE == kWhole) interleave<F, (FMT == kDecoded ? 1 : 3) + (BIAS ? 2 : 0)>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    for (int k = 0; k < steps; k += 2) {
+        step(k, std::integral_constant<int, 0>{});
+        step(k + 1, std::integral_constant<int, 1>{});
+    }
+
+    // Through LDS in fp32, 16 rows of a wave's quarter at a time, into octs of a row.
+    const int in8 = (g.in_cols + kOct - 1) / kOct * kOct;
+    float* strip = reinterpret_cast<float*>(smem) + wave * 16 * G::kWave;
+#pragma unroll
+    for (int m = 0; m < F; ++m) {
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < F; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) strip[(4 * (lane >> 4) + r) * G::kWave + 16 * n + (lane & 15)] = acc[m][n][r];
+        __syncthreads();
+        constexpr int kOctsW = G::kWave / kOct, kRows = 64 / kOctsW;
+#pragma unroll
+        for (int p = 0; p < 16 / kRows; ++p) {
+            const int r = p * kRows + lane / kOctsW;
+            const int oo = o0 + (wave >> 1) * G::kWave + 16 * m + r;
+            const int c = i0 + (wave & 1) * G::kWave + (lane % kOctsW) * kOct;
+            if (oo >= g.out_cols || c >= g.in_cols) continue;
+            const f4* src = reinterpret_cast<const f4*>(strip + r * G::kWave + (lane % kOctsW) * kOct);
+            const f4 lo = src[0], hi = src[1];
+            if (g.splits > 1) {
+                f4* dst = reinterpret_cast<f4*>(g.partials + (int64_t(split) * g.out_cols + oo) * in8 + c);
+                dst[0] = lo;
+                dst[1] = hi;
+                continue;
+            }
+            float v[kOct] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint16_t* out = g.dweight + int64_t(oo) * g.in_cols;
+            if (g.accumulate) {
+                float old[kOct];
+                widen_oct<DT>(load_oct(out, c, g.in_cols), old);
+#pragma unroll
+                for (int k = 0; k < kOct; ++k) v[k] += old[k];
+            }
+            store_oct(out, c, g.in_cols, narrow_oct<DT>(v));
         }
     }
+    if (!BIAS || g.dbias == nullptr || i0 != 0) return;
+    // The threads of a column's octs, added in row order.
     __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int k = 0; k < kOct; ++k) sums[row * TILE + oct * kOct + k] = bsum[k];
+    __syncthreads();
+    const int oo = o0 + tid;
+    if (tid >= TILE || oo >= g.out_cols) return;
+    float total = sums[tid];
+    for (int r = 1; r < G::kRowsPerPass; ++r) total += sums[r * TILE + tid];
+    if (g.splits > 1) {
+        g.bias_partials[int64_t(split) * g.out_cols + oo] = total;
+        return;
+    }
+    if (g.accumulate) total += widen<DT>(g.dbias[oo]);
+    g.dbias[oo] = static_cast<uint16_t>(narrow<DT>(total));
 }
 
 // Blocks are dispatched round-robin to the 8 XCDs; each XCD takes a contiguous
-// run of tiles, ordered so that about 32 tiles in flight form a patch of 8
-// output tiles by 4 input tiles that share operand panels in its L2.
+// run of tiles, ordered so that the 32 tiles in flight (one per CU) form a patch of
+// 4 output tiles by 8 input tiles that share operand panels in its L2 (8 by 4 was
+// 1.5% slower at 16384 tokens, 4096 -> 16384).
 __device__ __forceinline__ void place_tile(int id, int count, int out_tiles, int in_tiles, int& o, int& i) {
-    constexpr int kXcds = 8, kGroup = 8;
+    constexpr int kXcds = 8, kGroup = 4;
     const int per = count / kXcds, extra = count % kXcds;
     const int x = id % kXcds, k = id / kXcds;
     const int t = x * per + (x < extra ? x : extra) + k;
@@ -253,7 +335,6 @@ __device__ __forceinline__ void place_tile(int id, int count, int out_tiles, int
 template <int DT, int FMT, int TILE>
 __global__ __launch_bounds__(kGradThreads) void weight_grad_kernel(GradArgs g) {
     using G = GradTile<TILE>;
-    constexpr int F = G::kFrags;
     __shared__ __attribute__((aligned(16))) char smem[2 * G::kStageBytes];
     const int tiles = g.in_tiles * g.out_tiles;
     const int split = blockIdx.x / tiles;
@@ -262,86 +343,14 @@ __global__ __launch_bounds__(kGradThreads) void weight_grad_kernel(GradArgs g) {
     const int o0 = ot * TILE, i0 = in * TILE;
     const int64_t t0 = split * g.split_rows;
     const int64_t t_end = t0 + g.split_rows < g.rows ? t0 + g.split_rows : g.rows;
-    f16v acc[F][F];
-#pragma unroll
-    for (int m = 0; m < F; ++m)
-#pragma unroll
-        for (int n = 0; n < F; ++n) acc[m][n] = f16v{};
-    float bsum[kOct] = {};
-    const bool bias = g.dbias != nullptr && in == 0;
-    // Tiles that lie inside the operands take the unguarded loads, with 32-bit
-    // offsets within 64 tokens; the last tokens and the edges the guarded ones.
-    const bool inside = o0 + TILE <= g.out_cols && i0 + TILE <= g.pitch && g.dy_stride < (int64_t(1) << 24) &&
-                        g.pitch < (int64_t(1) << 24);
-    const int all = int((t_end - t0 + kTokens - 1) / kTokens);
-    const int whole = inside ? int((t_end - t0) / kTokens) : 0;
-    if (whole > 0) {
-        if (bias)
-            grad_loop<DT, FMT, TILE, kWhole, true>(g, smem, o0, i0, t0, whole, t_end, bsum, acc);
-        else
-            grad_loop<DT, FMT, TILE, kWhole, false>(g, smem, o0, i0, t0, whole, t_end, bsum, acc);
-    }
-    if (all > whole)
-        grad_loop<DT, FMT, TILE, kGuarded, true>(g, smem, o0, i0, t0 + int64_t(whole) * kTokens, all - whole, t_end, bsum,
-                                                 acc);
-
-    // Through LDS in fp32, 32 rows of a wave's quarter at a time, into octs of a row.
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int in8 = (g.in_cols + kOct - 1) / kOct * kOct;
-    float* strip = reinterpret_cast<float*>(smem) + wave * 32 * G::kWave;
-#pragma unroll
-    for (int m = 0; m < F; ++m) {
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < F; ++n)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                strip[(8 * (r / 4) + 4 * (lane >> 5) + r % 4) * G::kWave + 32 * n + (lane & 31)] = acc[m][n][r];
-        __syncthreads();
-        constexpr int kOctsW = G::kWave / kOct, kRows = 64 / kOctsW;
-#pragma unroll
-        for (int p = 0; p < 32 / kRows; ++p) {
-            const int r = p * kRows + lane / kOctsW;
-            const int o = o0 + (wave >> 1) * G::kWave + 32 * m + r;
-            const int c = i0 + (wave & 1) * G::kWave + (lane % kOctsW) * kOct;
-            if (o >= g.out_cols || c >= g.in_cols) continue;
-            const f4* src = reinterpret_cast<const f4*>(strip + r * G::kWave + (lane % kOctsW) * kOct);
-            const f4 lo = src[0], hi = src[1];
-            if (g.splits > 1) {
-                f4* dst = reinterpret_cast<f4*>(g.partials + (int64_t(split) * g.out_cols + o) * in8 + c);
-                dst[0] = lo;
-                dst[1] = hi;
-                continue;
-            }
-            float v[kOct] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            uint16_t* out = g.dweight + int64_t(o) * g.in_cols;
-            if (g.accumulate) {
-                float old[kOct];
-                widen_oct<DT>(load_oct(out, c, g.in_cols), old);
-#pragma unroll
-                for (int k = 0; k < kOct; ++k) v[k] += old[k];
-            }
-            store_oct(out, c, g.in_cols, narrow_oct<DT>(v));
-        }
-    }
-    if (!bias) return;
-    // The threads of a column's octs, added in row order.
-    __syncthreads();
-    float* sums = reinterpret_cast<float*>(smem);
-    const int oct = tid % G::kOcts, row = tid / G::kOcts;
-#pragma unroll
-    for (int k = 0; k < kOct; ++k) sums[row * TILE + oct * kOct + k] = bsum[k];
-    __syncthreads();
-    const int o = o0 + tid;
-    if (tid >= TILE || o >= g.out_cols) return;
-    float total = sums[tid];
-    for (int r = 1; r < G::kRowsPerPass; ++r) total += sums[r * TILE + tid];
-    if (g.splits > 1) {
-        g.bias_partials[int64_t(split) * g.out_cols + o] = total;
-        return;
-    }
-    if (g.accumulate) total += widen<DT>(g.dbias[o]);
-    g.dbias[o] = static_cast<uint16_t>(narrow<DT>(total));
+    const bool whole = t_end - t0 >= 4 * kTokens && g.in_cols > 0 && g.dy_stride >= kOct && g.dy_stride < (int64_t(1) << 24) &&
+                       g.pitch < (int64_t(1) << 24);
+    if (!whole)
+        grad_tile<DT, FMT, TILE, kGuarded, true>(g, smem, o0, i0, t0, t_end, split);
+    else if (g.dbias != nullptr && in == 0)
+        grad_tile<DT, FMT, TILE, kWhole, true>(g, smem, o0, i0, t0, t_end, split);
+    else
+        grad_tile<DT, FMT, TILE, kWhole, false>(g, smem, o0, i0, t0, t_end, split);
 }
 
 // Adds the splits' partial gradients in split order; an oct per thread.  The
@@ -388,9 +397,17 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(GradArgs g) {
 struct GradShape {
     int tile, in_tiles, out_tiles, splits;
     int64_t split_rows;
+    bool decode;  // restore the input first
 };
 
 constexpr int kCus = 256;
+// Restoring the input first costs a launch (3 us) and 3 bytes per element, and saves
+// every output tile the decoding, which draws issue slots and power from the matrix
+// units.  Measured without and with (us): 16384 tokens 4096 -> 16384 1994 / 1716;
+// 4096 tokens 1600 -> 6400 135 / 116; 2048 tokens 4096 -> 4096 69 / 68; 512 tokens
+// 4096 -> 4096 28 / 31; 48 tokens 1600 -> 4800 9 / 11; 16384 tokens 512 -> 512 32 / 40.
+constexpr int kDecodeTiles = 8;
+constexpr int64_t kDecodeProducts = 10000000000;
 
 inline GradShape grad_shape(int64_t rows, int64_t in_cols, int64_t out_cols) {
     const auto tiles = [&](int tile) {
@@ -401,10 +418,11 @@ inline GradShape grad_shape(int64_t rows, int64_t in_cols, int64_t out_cols) {
     s.in_tiles = int(std::max<int64_t>(1, ceil_div(in_cols, int64_t(s.tile))));
     s.out_tiles = int(ceil_div(out_cols, int64_t(s.tile)));
     const int64_t n = tiles(s.tile), steps = std::max<int64_t>(1, ceil_div(rows, int64_t(kTokens)));
-    // few tiles and many tokens: enough splits for two blocks per CU, of at least 8 staged tiles each
-    int64_t want = n >= kCus ? 1 : std::min(ceil_div(2 * kCus, n), std::max<int64_t>(1, steps / 8));
+    // few tiles and many tokens: enough splits for two blocks per CU, of at least 16 staged tiles each
+    int64_t want = n >= kCus ? 1 : std::min(ceil_div(2 * kCus, n), std::max<int64_t>(1, steps / 16));
     s.split_rows = ceil_div(steps, want) * kTokens;
     s.splits = int(std::max<int64_t>(1, ceil_div(rows, s.split_rows)));
+    s.decode = s.out_tiles >= kDecodeTiles && rows > 0 && in_cols * out_cols >= kDecodeProducts / rows;
     return s;
 }
 
@@ -417,10 +435,16 @@ inline int64_t partial_floats(const GradShape& s, int64_t in_cols, int64_t out_c
     return s.splits > 1 ? int64_t(s.splits) * out_cols * ceil_div(in_cols, int64_t(kOct)) * kOct : 0;
 }
 
+inline int64_t decoded_bytes(const GradShape& s, int64_t rows, int64_t in_cols) {
+    return s.decode ? 2 * rows * act_pitch(in_cols) : 0;
+}
+
+// The restored input, if there is one, then the partial gradients.
 inline int64_t weight_grad_workspace(int64_t rows, int64_t in_cols, int64_t out_cols) {
     if (rows == 0 || out_cols == 0) return 0;
     const GradShape s = grad_shape(rows, in_cols, out_cols);
-    return s.splits > 1 ? 4 * (partial_floats(s, in_cols, out_cols) + s.splits * out_cols) : 0;
+    return decoded_bytes(s, rows, in_cols) +
+           (s.splits > 1 ? 4 * (partial_floats(s, in_cols, out_cols) + s.splits * out_cols) : 0);
 }
 
 }  // namespace
@@ -468,16 +492,22 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const voi
     if ((rows == 0 && accumulate) || (in_cols == 0 && dbias == nullptr)) return ok();
     hipStream_t s = static_cast<hipStream_t>(stream);
     const GradShape sh = grad_shape(rows, in_cols, out_cols);
-    float* partials = static_cast<float*>(workspace);
-    const GradArgs args{in16(dy), dy_stride, in8(codes), pitch, scales, int(bpr), rows, int(in_cols), int(out_cols),
-                        sh.in_tiles, sh.out_tiles, sh.splits, sh.split_rows, accumulate, out16(dweight), out16(dbias),
-                        partials, sh.splits > 1 ? partials + partial_floats(sh, in_cols, out_cols) : nullptr};
+    char* ws = static_cast<char*>(workspace);
+    float* partials = reinterpret_cast<float*>(ws + decoded_bytes(sh, rows, in_cols));
+    if (sh.decode)
+        if (int rc = zero_act_restore(codes, scales, format, rows, in_cols, ws, pitch, dtype, stream)) return rc;
+    const GradArgs args{in16(dy), dy_stride, sh.decode ? in8(ws) : in8(codes), sh.decode ? 2 * pitch : pitch, scales,
+                        int(bpr), rows, int(in_cols), int(out_cols), sh.in_tiles, sh.out_tiles, sh.splits,
+                        sh.split_rows, accumulate, out16(dweight), out16(dbias), partials,
+                        sh.splits > 1 ? partials + partial_floats(sh, in_cols, out_cols) : nullptr};
     const dim3 grid(unsigned(int64_t(sh.in_tiles) * sh.out_tiles * sh.splits));
-    hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
+    const auto run = [&](auto dt, auto fmt) {
         constexpr int D = decltype(dt)::value, M = decltype(fmt)::value;
         return sh.tile == 256 ? launch(weight_grad_kernel<D, M, 256>, grid, dim3(kGradThreads), s, args)
                               : launch(weight_grad_kernel<D, M, 128>, grid, dim3(kGradThreads), s, args);
-    });
+    };
+    hipError_t e = sh.decode ? with_dtype(dtype, [&](auto dt) { return run(dt, std::integral_constant<int, kDecoded>{}); })
+                             : with_types(dtype, format, run);
     if (e != hipSuccess || sh.splits <= 1) return hip_status(e, fn);
     const int64_t threads = ceil_div(in_cols, int64_t(kOct)) * out_cols + (dbias != nullptr ? out_cols : 0);
     e = with_dtype(dtype, [&](auto dt) {
