@@ -163,14 +163,14 @@ class _Fake:
 
     def __init__(self, shape, stride, index=0, size=2, room=None, offset=0):
         self.shape, self._stride, self._size, self._offset = shape, stride, size, offset
-        self.device = type("D", (), {"index": index})()
+        self._index = index
         self._room = room if room is not None else offset + (shape[0] - 1) * stride[0] + shape[-1]
 
-    def dim(self):
-        return len(self.shape)
+    def get_device(self):
+        return self._index
 
-    def stride(self, d):
-        return self._stride[d]
+    def stride(self):
+        return self._stride
 
     def element_size(self):
         return self._size
@@ -190,9 +190,10 @@ class _Fake:
     (_Fake((R, C), (C, 1), size=4), "16-bit"),
     (_Fake((R, C), (C, 2)), "adjacent"),
     (_Fake((R, C), (C + 2, 1)), "apart"),
-    (_Fake((R, C), (C, 1), room=R * C - 1), "holds"),
+    (_Fake((R - 1, C), (C, 1)), "holds"),
+    (_Fake((R * C - 1,), (1,), room=R * C - 1), "holds"),
 ])
 def test_matrices_are_checked(monkeypatch, fake, match):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(abi, "_device", lambda: 0)
     with pytest.raises(ValueError, match=match):
         _save(x=fake)

@@ -237,21 +237,28 @@ def _nbytes(x):
     return x.numel() * x.element_size()
 
 
+_DTYPES = {"f16": ZERO_F16, "bf16": ZERO_BF16, "torch.float16": ZERO_F16, "torch.bfloat16": ZERO_BF16}
+
+
 def _dtype(d):
     if isinstance(d, int):
         return d                      # validated by the library
-    name = str(d)
-    table = {"f16": ZERO_F16, "bf16": ZERO_BF16, "torch.float16": ZERO_F16,
-             "torch.bfloat16": ZERO_BF16}
-    if name in table:
-        return table[name]
+    if not isinstance(d, str):
+        d = str(d)
+    if d in _DTYPES:
+        return _DTYPES[d]
     raise ValueError(f"not a 16-bit dtype: {d!r}")
+
+
+# The current stream's handle without building a Stream object (a microsecond per call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -579,41 +586,59 @@ def zero_gather_dequant(plan, code_shards, scale_shards, unit_begin, unit_end, b
 # 8-bit activation checkpoints
 # ---------------------------------------------------------------------------
 
-def _need_here(x, nbytes, what):
-    """_need, and on the current device (the call's stream belongs to it)."""
-    if x is None or isinstance(x, int) or nbytes <= 0:
-        return
-    _need(x, nbytes, what)
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on device {x.device.index}, the current one is {torch.cuda.current_device()}")
-
-
-def _need_matrix(x, rows, cols, stride, what):
-    """A tensor argument must be a 16-bit device matrix whose memory holds `rows` rows of `cols` adjacent
-    values, `stride` apart (a view into a larger matrix will do)."""
-    if x is None or isinstance(x, int) or rows <= 0 or cols <= 0:
-        return
+def _elsewhere(x, dev, what):
     if not x.is_cuda:
         raise ValueError(f"{what} must be a device tensor")
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on device {x.device.index}, the current one is {torch.cuda.current_device()}")
+    raise ValueError(f"{what} is on device {x.get_device()}, the current one is {dev}")
+
+
+def _need_here(x, nbytes, dev, what):
+    """_need, and on the current device `dev` (the call's stream belongs to it)."""
+    if x is None or isinstance(x, int) or nbytes <= 0:
+        return
+    if x.get_device() != dev:
+        _elsewhere(x, dev, what)
+    _need(x, nbytes, what)
+
+
+def _need_matrix(x, rows, cols, stride, dev, what):
+    """A tensor argument must be a 16-bit matrix on the current device whose memory holds `rows` rows of
+    `cols` adjacent values, `stride` apart (a view into a larger matrix will do)."""
+    if x is None or isinstance(x, int) or rows <= 0 or cols <= 0:
+        return
+    if x.get_device() != dev:
+        _elsewhere(x, dev, what)
     if x.element_size() != 2:
         raise ValueError(f"{what} must hold 16-bit values")
-    if x.dim() > 0 and x.shape[-1] > 1 and x.stride(-1) != 1:
+    shape, strides = x.shape, x.stride()
+    if len(shape) == 2 and strides == (stride, 1) and shape[0] >= rows and shape[1] >= cols:
+        return
+    if len(shape) > 0 and shape[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{what}'s columns must be adjacent")
-    if x.dim() == 2 and x.shape[0] > 1 and x.stride(0) != stride:
-        raise ValueError(f"{what}'s rows are {x.stride(0)} apart, not {stride}")
+    if len(shape) == 2 and shape[0] > 1 and strides[0] != stride:
+        raise ValueError(f"{what}'s rows are {strides[0]} apart, not {stride}")
     have = x.untyped_storage().nbytes() // 2 - x.storage_offset()
     need = (rows - 1) * stride + cols
     if have < need:
         raise ValueError(f"{what} holds {have} values, needs {need}")
 
 
-def _need_checkpoint(codes, scales, rows, cols, what=""):
+def _need_checkpoint(codes, scales, rows, cols, dev, what=""):
     # sizes out of range are the library's to report
     pitch = (cols + 15) // 16 * 16
-    _need_here(codes, rows * pitch, f"{what}codes")
-    _need_here(scales, 4 * rows * ((cols + ZERO_QBLOCK - 1) // ZERO_QBLOCK), f"{what}scales")
+    _need_here(codes, rows * pitch, dev, what + "codes")
+    _need_here(scales, 4 * rows * ((cols + ZERO_QBLOCK - 1) // ZERO_QBLOCK), dev, what + "scales")
+
+
+_have_gpu = None
+
+
+def _device():
+    """The current device, or None without one (every tensor is then refused as no device tensor)."""
+    global _have_gpu
+    if _have_gpu is None:
+        _have_gpu = torch.cuda.is_available()
+    return torch.cuda.current_device() if _have_gpu else None
 
 
 def zero_act_code_bytes(rows, cols):
@@ -631,26 +656,29 @@ def zero_act_scale_count(rows, cols):
 
 
 def zero_act_save(x, x_stride, dtype, rows, cols, format, codes, scales, stream=None):
-    _need_matrix(x, rows, cols, x_stride, "x")
-    _need_checkpoint(codes, scales, rows, cols)
+    dev = _device()
+    _need_matrix(x, rows, cols, x_stride, dev, "x")
+    _need_checkpoint(codes, scales, rows, cols, dev)
     _check(lib.zero_act_save(_ptr(x), int(x_stride), _dtype(dtype), int(rows), int(cols), int(format), _ptr(codes),
                              _ptr(scales), _stream(stream)))
 
 
 def zero_act_restore(codes, scales, format, rows, cols, y, y_stride, dtype, stream=None):
-    _need_checkpoint(codes, scales, rows, cols)
-    _need_matrix(y, rows, cols, y_stride, "y")
+    dev = _device()
+    _need_checkpoint(codes, scales, rows, cols, dev)
+    _need_matrix(y, rows, cols, y_stride, dev, "y")
     _check(lib.zero_act_restore(_ptr(codes), _ptr(scales), int(format), int(rows), int(cols), _ptr(y), int(y_stride),
                                 _dtype(dtype), _stream(stream)))
 
 
 def zero_act_glu_forward(gate, gate_stride, up, up_stride, dtype, rows, cols, fn, format, h, h_stride, gate_codes,
                          gate_scales, up_codes, up_scales, stream=None):
-    _need_matrix(gate, rows, cols, gate_stride, "gate")
-    _need_matrix(up, rows, cols, up_stride, "up")
-    _need_matrix(h, rows, cols, h_stride, "h")
-    _need_checkpoint(gate_codes, gate_scales, rows, cols, "gate_")
-    _need_checkpoint(up_codes, up_scales, rows, cols, "up_")
+    dev = _device()
+    _need_matrix(gate, rows, cols, gate_stride, dev, "gate")
+    _need_matrix(up, rows, cols, up_stride, dev, "up")
+    _need_matrix(h, rows, cols, h_stride, dev, "h")
+    _need_checkpoint(gate_codes, gate_scales, rows, cols, dev, "gate_")
+    _need_checkpoint(up_codes, up_scales, rows, cols, dev, "up_")
     _check(lib.zero_act_glu_forward(_ptr(gate), int(gate_stride), _ptr(up), int(up_stride), _dtype(dtype), int(rows),
                                     int(cols), int(fn), int(format), _ptr(h), int(h_stride), _ptr(gate_codes),
                                     _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), _stream(stream)))
@@ -658,12 +686,13 @@ def zero_act_glu_forward(gate, gate_stride, up, up_stride, dtype, rows, cols, fn
 
 def zero_act_glu_backward(gate_codes, gate_scales, up_codes, up_scales, format, rows, cols, fn, dh, dh_stride, dtype,
                           dgate, dgate_stride, dup, dup_stride, h=None, h_stride=0, stream=None):
-    _need_checkpoint(gate_codes, gate_scales, rows, cols, "gate_")
-    _need_checkpoint(up_codes, up_scales, rows, cols, "up_")
-    _need_matrix(dh, rows, cols, dh_stride, "dh")
-    _need_matrix(dgate, rows, cols, dgate_stride, "dgate")
-    _need_matrix(dup, rows, cols, dup_stride, "dup")
-    _need_matrix(h, rows, cols, h_stride, "h")
+    dev = _device()
+    _need_checkpoint(gate_codes, gate_scales, rows, cols, dev, "gate_")
+    _need_checkpoint(up_codes, up_scales, rows, cols, dev, "up_")
+    _need_matrix(dh, rows, cols, dh_stride, dev, "dh")
+    _need_matrix(dgate, rows, cols, dgate_stride, dev, "dgate")
+    _need_matrix(dup, rows, cols, dup_stride, dev, "dup")
+    _need_matrix(h, rows, cols, h_stride, dev, "h")
     _check(lib.zero_act_glu_backward(_ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), int(format),
                                      int(rows), int(cols), int(fn), _ptr(dh), int(dh_stride), _dtype(dtype),
                                      _ptr(dgate), int(dgate_stride), _ptr(dup), int(dup_stride), _ptr(h),
@@ -672,16 +701,17 @@ def zero_act_glu_backward(gate_codes, gate_scales, up_codes, up_scales, format, 
 
 def zero_act_norm_forward(x, x_stride, branch, branch_stride, alpha, weight, bias, dtype, rows, cols, kind, eps, format,
                           res, res_stride, y, y_stride, codes, scales, mean, rstd, stream=None):
-    _need_matrix(x, rows, cols, x_stride, "x")
-    _need_matrix(branch, rows, cols, branch_stride, "branch")
-    _need_matrix(res, rows, cols, res_stride, "res")
-    _need_matrix(y, rows, cols, y_stride, "y")
-    _need_checkpoint(codes, scales, rows, cols)
+    dev = _device()
+    _need_matrix(x, rows, cols, x_stride, dev, "x")
+    _need_matrix(branch, rows, cols, branch_stride, dev, "branch")
+    _need_matrix(res, rows, cols, res_stride, dev, "res")
+    _need_matrix(y, rows, cols, y_stride, dev, "y")
+    _need_checkpoint(codes, scales, rows, cols, dev)
     if rows > 0:
-        _need_here(weight, 2 * cols, "weight")
-        _need_here(bias, 2 * cols, "bias")
-    _need_here(mean, 4 * rows, "mean")
-    _need_here(rstd, 4 * rows, "rstd")
+        _need_here(weight, 2 * cols, dev, "weight")
+        _need_here(bias, 2 * cols, dev, "bias")
+    _need_here(mean, 4 * rows, dev, "mean")
+    _need_here(rstd, 4 * rows, dev, "rstd")
     _check(lib.zero_act_norm_forward(_ptr(x), int(x_stride), _ptr(branch), int(branch_stride), float(alpha),
                                      _ptr(weight), _ptr(bias), _dtype(dtype), int(rows), int(cols), int(kind),
                                      float(eps), int(format), _ptr(res), int(res_stride), _ptr(y), int(y_stride),
@@ -698,17 +728,18 @@ def zero_act_norm_workspace_bytes(rows, cols):
 def zero_act_norm_backward(codes, scales, format, mean, rstd, weight, rows, cols, kind, dy, dy_stride, dres,
                            dres_stride, alpha, dtype, dx, dx_stride, dbranch, dbranch_stride, accumulate, dweight,
                            dbias, workspace, stream=None, workspace_bytes=None):
+    dev = _device()
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    _need_checkpoint(codes, scales, rows, cols)
-    _need_here(mean, 4 * rows, "mean")
-    _need_here(rstd, 4 * rows, "rstd")
-    _need_here(weight, 2 * cols, "weight")
+    _need_checkpoint(codes, scales, rows, cols, dev)
+    _need_here(mean, 4 * rows, dev, "mean")
+    _need_here(rstd, 4 * rows, dev, "rstd")
+    _need_here(weight, 2 * cols, dev, "weight")
     for t, stride, what in ((dy, dy_stride, "dy"), (dres, dres_stride, "dres"), (dx, dx_stride, "dx"),
                             (dbranch, dbranch_stride, "dbranch")):
-        _need_matrix(t, rows, cols, stride, what)
-    _need_here(dweight, 2 * cols, "dweight")
-    _need_here(dbias, 2 * cols, "dbias")
-    _need_here(workspace, wb, "workspace")
+        _need_matrix(t, rows, cols, stride, dev, what)
+    _need_here(dweight, 2 * cols, dev, "dweight")
+    _need_here(dbias, 2 * cols, dev, "dbias")
+    _need_here(workspace, wb, dev, "workspace")
     _check(lib.zero_act_norm_backward(_ptr(codes), _ptr(scales), int(format), _ptr(mean), _ptr(rstd), _ptr(weight),
                                       int(rows), int(cols), int(kind), _ptr(dy), int(dy_stride), _ptr(dres),
                                       int(dres_stride), float(alpha), _dtype(dtype), _ptr(dx), int(dx_stride),
@@ -725,12 +756,13 @@ def zero_act_weight_grad_workspace_bytes(rows, in_cols, out_cols):
 
 def zero_act_weight_grad(dy, dy_stride, dtype, codes, scales, format, rows, in_cols, out_cols, accumulate, dweight,
                          dbias, workspace, stream=None, workspace_bytes=None):
+    dev = _device()
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    _need_matrix(dy, rows, out_cols, dy_stride, "dy")
-    _need_checkpoint(codes, scales, rows, in_cols)
-    _need_here(dweight, 2 * in_cols * out_cols, "dweight")
-    _need_here(dbias, 2 * out_cols, "dbias")
-    _need_here(workspace, wb, "workspace")
+    _need_matrix(dy, rows, out_cols, dy_stride, dev, "dy")
+    _need_checkpoint(codes, scales, rows, in_cols, dev)
+    _need_here(dweight, 2 * in_cols * out_cols, dev, "dweight")
+    _need_here(dbias, 2 * out_cols, dev, "dbias")
+    _need_here(workspace, wb, dev, "workspace")
     _check(lib.zero_act_weight_grad(_ptr(dy), int(dy_stride), _dtype(dtype), _ptr(codes), _ptr(scales), int(format),
                                     int(rows), int(in_cols), int(out_cols), int(bool(accumulate)), _ptr(dweight),
                                     _ptr(dbias), _ptr(workspace), wb, _stream(stream)))
