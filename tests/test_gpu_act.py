@@ -344,6 +344,36 @@ def test_norm(abi, kind, dtype, fmt, rows, cols):
     assert dx.guards_intact()
 
 
+# A block of the backward pass does several rows: at each number of threads per row, aligned and not.
+@pytest.mark.parametrize("kind,dtype,fmt", [("rms", "bf16", "int8"), ("layer", "f16", "e4m3")])
+@pytest.mark.parametrize("rows,cols", [(4500, 300), (1500, 601), (600, 2104), (530, 5001), (520, 9000)])
+def test_norm_many_rows(abi, kind, dtype, fmt, rows, cols):
+    test_norm(abi, kind, dtype, fmt, rows, cols)
+
+
+def test_norm_wants_only_some_gradients(abi):
+    rows, cols = 700, 1031
+    rng = np.random.default_rng(2)
+    x, dy = activation(rng, rows, cols, "bf16"), activation(rng, rows, cols, "bf16", 0.1)
+    codes, scales = _dev_ckpt(*act.save(x, "bf16", "int8"))
+    rstd = torch.rand(rows, device="cuda") + 0.5
+    md = Mat(rows, cols, "bf16", dy)
+    ws = torch.empty(abi.zero_act_norm_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    out = {}
+    for w, b in ((True, True), (True, False), (False, True), (False, False)):
+        ws.fill_(0xFF)
+        dx, gw, gb = Mat(rows, cols, "bf16"), Mat(1, cols, "bf16"), Mat(1, cols, "bf16")
+        abi.zero_act_norm_backward(codes, scales, 1, None, rstd, None, rows, cols, 1, md.t, cols, None, 0, 1.0, "bf16",
+                                   dx.t, cols, None, 0, False, gw.t if w else None, gb.t if b else None, ws)
+        torch.cuda.synchronize()
+        out[w, b] = dx.bits(), gw.bits(), gb.bits()
+    ref = out[True, True]
+    for (w, b), got in out.items():
+        assert np.array_equal(got[0], ref[0])
+        assert np.array_equal(got[1], ref[1]) if w else (got[1] == 0x5A5A).all()
+        assert np.array_equal(got[2], ref[2]) if b else (got[2] == 0x5A5A).all()
+
+
 def test_norm_in_place(abi):
     # the residual stream and its gradient updated in place give the same bits as out of place
     rows, cols = 21, 3000

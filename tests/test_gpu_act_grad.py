@@ -85,6 +85,64 @@ def test_integers_are_exact(abi):
         assert np.array_equal(mb.bits()[0], rounding.narrow(dy.sum(0).astype(np.float32), "bf16"))
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,inner,outer", [
+    (200, 4100, 4104),     # 256 x 256 tiles, decoded while staged
+    (700, 4100, 4101),     # ... restored first; rows of odd length
+    (4801, 1030, 2056),    # 128 x 128 tiles, restored first, split over the tokens
+    (130, 520, 70_000),    # one row of input tiles
+    (40_000, 120, 9),      # one tile, many splits, fewer than a quarter of it used
+])
+def test_large_shapes_are_exact(abi, dtype, fmt, rows, inner, outer):
+    # Integers as above (E4M3 holds those up to 16 with a block maximum of 448), checked in fp64 on the GPU.
+    _note(f"weight_grad exact {dtype} {fmt} {rows} {inner} {outer}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(rows)
+    half = TORCH16[dtype]
+    x = torch.randint(-9, 10, (rows, inner), generator=gen, device="cuda").to(half)
+    x[:, ::256] = 127 if fmt == "int8" else 448
+    dy = torch.randint(-1, 2, (rows, outer), generator=gen, device="cuda").to(half)
+    codes = torch.empty(rows, (inner + 15) // 16 * 16, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(rows, -(-inner // 256), device="cuda")
+    abi.zero_act_save(x, inner, dtype, rows, inner, FMT[fmt], codes, scales)
+    mw, mb = Mat(outer, inner, dtype, off=1), Mat(1, outer, dtype, off=3)
+    ws = torch.empty(max(abi.zero_act_weight_grad_workspace_bytes(rows, inner, outer), 16), dtype=torch.uint8,
+                     device="cuda").fill_(0xFF)
+    abi.zero_act_weight_grad(dy, outer, dtype, codes, scales, FMT[fmt], rows, inner, outer, False, mw.view.view(-1),
+                             mb.view.view(-1), ws)
+    want = dy.double().t().contiguous() @ x.double()
+    torch.cuda.synchronize()
+    assert bool((scales == 1).all()) and float(want.abs().max()) < 2 ** 24
+    assert torch.equal(mw.t, want.float().to(half)) and torch.equal(mb.t[0], dy.double().sum(0).float().to(half))
+    assert mw.guards_intact() and mb.guards_intact()
+
+
+def test_rows_far_apart(abi):
+    # A stride past the 24 bits of the unchecked loads' offsets.
+    rows, inner, outer, stride = 130, 40, 24, (1 << 24) + 8
+    big = torch.zeros((rows - 1) * stride + outer, dtype=torch.bfloat16, device="cuda")
+    dy = torch.randint(-3, 4, (rows, outer), device="cuda").to(torch.bfloat16)
+    view = big.as_strided((rows, outer), (stride, 1))
+    view.copy_(dy)
+    codes = torch.randint(-127, 128, (rows, 48), dtype=torch.int8, device="cuda").view(torch.uint8)
+    scales = torch.ones(rows, 1, device="cuda")
+    dw = torch.empty(outer, inner, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(abi.zero_act_weight_grad_workspace_bytes(rows, inner, outer), 16), dtype=torch.uint8, device="cuda")
+    abi.zero_act_weight_grad(view, stride, "bf16", codes, scales, 1, rows, inner, outer, False, dw, None, ws)
+    want = dy.double().t().contiguous() @ codes.view(torch.int8)[:, :inner].double()
+    torch.cuda.synchronize()
+    assert torch.equal(dw, want.float().to(torch.bfloat16))
+
+
+def test_narrow_gradients_of_many_tokens(abi):
+    # Fewer output columns than an oct, rows closer than an oct: every load is checked.
+    for outer in (1, 3, 7, 8, 9):
+        rng = np.random.default_rng(outer)
+        x, dy = activation(rng, 333, 300, "f16"), activation(rng, 333, outer, "f16", 0.1)
+        _check(*_run(abi, "f16", "int8", x, dy), "f16")
+
+
 def test_non_finite_values_reach_the_gradient(abi):
     rng = np.random.default_rng(3)
     x, dy = activation(rng, 300, 600, "bf16"), activation(rng, 300, 70, "bf16")
@@ -113,6 +171,12 @@ def test_subnormals_count(abi):
     tiny = np.full((40, 256), 0x007F, np.uint16)               # 127 * 2^-24: scale 2^-24, restored exactly
     mw, _, _, _ = _run(abi, "f16", "int8", tiny, big)
     assert np.array_equal(wide(mw.bits(), "f16"), np.full((64, 256), 40 * 1024 * 127 * 2.0 ** -24))
+    # the same in bf16: 2^-133 times 2^100
+    dy = np.full((40, 64), 0x0001, np.uint16)
+    x = np.full((40, 256), 0x7180, np.uint16)                  # 2^100
+    mw, _, _, _ = _run(abi, "bf16", "int8", x, dy)
+    got = wide(mw.bits(), "bf16")
+    assert np.all(np.abs(got / (40 * 2.0 ** -33) - 1) <= 2.0 ** -8), got[0, :3]
 
 
 def test_no_rows_no_columns(abi):
@@ -169,7 +233,7 @@ class Block:
     backward from the checkpoints of res, y, g, u and h; then the sharded step's reduce, norm and AdamW.
     """
 
-    T, H, F = 200, 264, 520
+    T, H, F = 1100, 264, 520
 
     def __init__(self, abi, seed):
         gen = torch.Generator(device="cuda")

@@ -167,52 +167,43 @@ __device__ __forceinline__ void act_eval(float g, float& f, float& df) {
 }
 
 // One pair of blocks per wave: 8192 x 16384 gated forward 171 us, with 2 180, with 4 186.
-constexpr int kGluPairs = 1;
-
 template <int DT, int FMT, int FN, bool GATED>
 __global__ __launch_bounds__(kActThreads) void glu_forward_kernel(
     const uint16_t* __restrict__ gate, int64_t gate_stride, const uint16_t* __restrict__ up, int64_t up_stride,
     int cols, uint32_t nblocks, FastDiv per_row, uint16_t* __restrict__ h, int64_t h_stride,
     uint8_t* __restrict__ gate_codes, float* __restrict__ gate_scales, uint8_t* __restrict__ up_codes,
     float* __restrict__ up_scales, int64_t pitch) {
-    u4 wg[kGluPairs], wu[kGluPairs];
-    Place p[kGluPairs];
-#pragma unroll
-    for (int k = 0; k < kGluPairs; ++k) {
-        p[k] = place_of<kGluPairs>(k, nblocks, per_row);
-        wg[k] = wu[k] = u4{0u, 0u, 0u, 0u};
-        if (p[k].live && p[k].col < cols) {
-            wg[k] = load_oct(gate + p[k].row * gate_stride, p[k].col, cols);
-            if constexpr (GATED) wu[k] = load_oct(up + p[k].row * up_stride, p[k].col, cols);
-        }
+    const Place p = place_of<1>(0, nblocks, per_row);
+    u4 wg{0u, 0u, 0u, 0u}, wu{0u, 0u, 0u, 0u};
+    if (p.live && p.col < cols) {
+        wg = load_oct(gate + p.row * gate_stride, p.col, cols);
+        if constexpr (GATED) wu = load_oct(up + p.row * up_stride, p.col, cols);
     }
+    const float gs = block_scale<DT, FMT>(wg);
+    float us = 0.0f;
+    if constexpr (GATED) us = block_scale<DT, FMT>(wu);
+    if (!p.live) return;
+    float g[kOct], u[kOct], o[kOct];
+    widen_oct<DT>(wg, g);
+    if constexpr (GATED) widen_oct<DT>(wu, u);
 #pragma unroll
-    for (int k = 0; k < kGluPairs; ++k) {
-        const float gs = block_scale<DT, FMT>(wg[k]);
-        float us = 0.0f;
-        if constexpr (GATED) us = block_scale<DT, FMT>(wu[k]);
-        if (!p[k].live) continue;
-        float g[kOct], u[kOct], o[kOct];
-        widen_oct<DT>(wg[k], g);
-        if constexpr (GATED) widen_oct<DT>(wu[k], u);
-#pragma unroll
-        for (int i = 0; i < kOct; ++i) {
-            float f, df;
-            act_eval<FN, false>(g[i], f, df);
-            o[i] = GATED ? f * u[i] : f;
-        }
-        if (p[k].col < cols) store_oct(h + p[k].row * h_stride, p[k].col, cols, narrow_oct<DT>(o));
-        if ((threadIdx.x & 31) == 0) {
-            gate_scales[p[k].block] = gs;
-            if constexpr (GATED) up_scales[p[k].block] = us;
-        }
-        if (p[k].col < pitch) {
-            store_codes(gate_codes + p[k].row * pitch, p[k].col, encode_oct<FMT>(g, gs));
-            if constexpr (GATED) store_codes(up_codes + p[k].row * pitch, p[k].col, encode_oct<FMT>(u, us));
-        }
+    for (int i = 0; i < kOct; ++i) {
+        float f, df;
+        act_eval<FN, false>(g[i], f, df);
+        o[i] = GATED ? f * u[i] : f;
+    }
+    if (p.col < cols) store_oct(h + p.row * h_stride, p.col, cols, narrow_oct<DT>(o));
+    if ((threadIdx.x & 31) == 0) {
+        gate_scales[p.block] = gs;
+        if constexpr (GATED) up_scales[p.block] = us;
+    }
+    if (p.col < pitch) {
+        store_codes(gate_codes + p.row * pitch, p.col, encode_oct<FMT>(g, gs));
+        if constexpr (GATED) store_codes(up_codes + p.row * pitch, p.col, encode_oct<FMT>(u, us));
     }
 }
 
+// 8192 x 16384 gated with h: 215 us, 5.6 TB/s.
 template <int DT, int FMT, int FN, bool GATED>
 __global__ __launch_bounds__(kActThreads) void glu_backward_kernel(
     const uint8_t* __restrict__ gate_codes, const float* __restrict__ gate_scales,
@@ -220,43 +211,29 @@ __global__ __launch_bounds__(kActThreads) void glu_backward_kernel(
     uint32_t nblocks, FastDiv per_row, const uint16_t* __restrict__ dh, int64_t dh_stride,
     uint16_t* __restrict__ dgate, int64_t dgate_stride, uint16_t* __restrict__ dup, int64_t dup_stride,
     uint16_t* __restrict__ h, int64_t h_stride) {
-    u4 wd[kGluPairs];
-    u2 qg[kGluPairs], qu[kGluPairs];
-    float sg[kGluPairs], su[kGluPairs];
-    Place p[kGluPairs];
-#pragma unroll
-    for (int k = 0; k < kGluPairs; ++k) {
-        p[k] = place_of<kGluPairs>(k, nblocks, per_row);
-        p[k].live = p[k].live && p[k].col < cols;
-        if (p[k].live) {
-            wd[k] = load_oct(dh + p[k].row * dh_stride, p[k].col, cols);
-            qg[k] = load_codes(gate_codes + p[k].row * pitch, p[k].col);
-            sg[k] = gate_scales[p[k].block];
-            if constexpr (GATED) {
-                qu[k] = load_codes(up_codes + p[k].row * pitch, p[k].col);
-                su[k] = up_scales[p[k].block];
-            }
-        }
+    const Place p = place_of<1>(0, nblocks, per_row);
+    if (!p.live || p.col >= cols) return;
+    const u4 wd = load_oct(dh + p.row * dh_stride, p.col, cols);
+    const u2 qg = load_codes(gate_codes + p.row * pitch, p.col);
+    const float sg = gate_scales[p.block];
+    float d[kOct], g[kOct], u[kOct], a[kOct], b[kOct], o[kOct];
+    if constexpr (GATED) {
+        const u2 qu = load_codes(up_codes + p.row * pitch, p.col);
+        widen_oct<DT>(decode_oct<DT, FMT>(qu, up_scales[p.block]), u);
     }
+    widen_oct<DT>(wd, d);
+    widen_oct<DT>(decode_oct<DT, FMT>(qg, sg), g);
 #pragma unroll
-    for (int k = 0; k < kGluPairs; ++k) {
-        if (!p[k].live) continue;
-        float d[kOct], g[kOct], u[kOct], a[kOct], b[kOct], o[kOct];
-        widen_oct<DT>(wd[k], d);
-        widen_oct<DT>(decode_oct<DT, FMT>(qg[k], sg[k]), g);
-        if constexpr (GATED) widen_oct<DT>(decode_oct<DT, FMT>(qu[k], su[k]), u);
-#pragma unroll
-        for (int i = 0; i < kOct; ++i) {
-            float f, df;
-            act_eval<FN, true>(g[i], f, df);
-            a[i] = (GATED ? d[i] * u[i] : d[i]) * df;
-            b[i] = d[i] * f;
-            o[i] = GATED ? f * u[i] : f;
-        }
-        store_oct(dgate + p[k].row * dgate_stride, p[k].col, cols, narrow_oct<DT>(a));
-        if constexpr (GATED) store_oct(dup + p[k].row * dup_stride, p[k].col, cols, narrow_oct<DT>(b));
-        if (h != nullptr) store_oct(h + p[k].row * h_stride, p[k].col, cols, narrow_oct<DT>(o));
+    for (int i = 0; i < kOct; ++i) {
+        float f, df;
+        act_eval<FN, true>(g[i], f, df);
+        a[i] = (GATED ? d[i] * u[i] : d[i]) * df;
+        b[i] = d[i] * f;
+        o[i] = GATED ? f * u[i] : f;
     }
+    store_oct(dgate + p.row * dgate_stride, p.col, cols, narrow_oct<DT>(a));
+    if constexpr (GATED) store_oct(dup + p.row * dup_stride, p.col, cols, narrow_oct<DT>(b));
+    if (h != nullptr) store_oct(h + p.row * h_stride, p.col, cols, narrow_oct<DT>(o));
 }
 
 // ---------------------------------------------------------------------------
@@ -717,8 +694,8 @@ int zero_act_restore(const void* codes, const float* scales, int format, int64_t
     const FastDiv per_row = fast_div(uint32_t(act_blocks(cols)));
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
-        return launch(act_restore_kernel<decltype(dt)::value, decltype(fmt)::value>, act_grid(nb, kRestorePairs), dim3(kActThreads), s, in8(codes),
-                      pitch, scales, int(cols), uint32_t(nb), per_row, out16(y), y_stride);
+        return launch(act_restore_kernel<decltype(dt)::value, decltype(fmt)::value>, act_grid(nb, kRestorePairs),
+                      dim3(kActThreads), s, in8(codes), pitch, scales, int(cols), uint32_t(nb), per_row, out16(y), y_stride);
     });
     return hip_status(e, fn);
 }
@@ -754,7 +731,8 @@ int zero_act_glu_forward(const void* gate, int64_t gate_stride, const void* up, 
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
         return with_fn(fn_id, gated, [&](auto f, auto g) {
-            return launch(glu_forward_kernel<decltype(dt)::value, decltype(fmt)::value, decltype(f)::value, decltype(g)::value>, act_grid(nb, kGluPairs), dim3(kActThreads), s,
+            constexpr int D = decltype(dt)::value, M = decltype(fmt)::value, N = decltype(f)::value;
+            return launch(glu_forward_kernel<D, M, N, decltype(g)::value>, act_grid(nb, 1), dim3(kActThreads), s,
                           in16(gate), gate_stride, in16(up), up_stride, int(cols), uint32_t(nb), per_row, out16(h),
                           h_stride, out8(gate_codes), gate_scales, out8(up_codes), up_scales, pitch);
         });
@@ -797,7 +775,8 @@ int zero_act_glu_backward(const void* gate_codes, const float* gate_scales, cons
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
         return with_fn(fn_id, gated, [&](auto f, auto g) {
-            return launch(glu_backward_kernel<decltype(dt)::value, decltype(fmt)::value, decltype(f)::value, decltype(g)::value>, act_grid(nb, kGluPairs), dim3(kActThreads), s,
+            constexpr int D = decltype(dt)::value, M = decltype(fmt)::value, N = decltype(f)::value;
+            return launch(glu_backward_kernel<D, M, N, decltype(g)::value>, act_grid(nb, 1), dim3(kActThreads), s,
                           in8(gate_codes), gate_scales, in8(up_codes), up_scales, pitch, int(cols), uint32_t(nb), per_row,
                           in16(dh), dh_stride, out16(dgate), dgate_stride, out16(dup), dup_stride, out16(h), h_stride);
         });
@@ -847,8 +826,9 @@ int zero_act_norm_forward(const void* x, int64_t x_stride, const void* branch, i
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
         return with_shape<true>(cols, [&](auto t, auto v) {
-            const dim3 grid{unsigned(ceil_div(rows, int64_t(norm_rows<decltype(t)::value>())))};
-            return launch(norm_forward_kernel<decltype(dt)::value, decltype(fmt)::value, decltype(t)::value, decltype(v)::value>, grid, dim3(norm_threads<decltype(t)::value>()), s, in16(x),
+            constexpr int D = decltype(dt)::value, M = decltype(fmt)::value, T = decltype(t)::value;
+            const dim3 grid{unsigned(ceil_div(rows, int64_t(norm_rows<T>())))};
+            return launch(norm_forward_kernel<D, M, T, decltype(v)::value>, grid, dim3(norm_threads<T>()), s, in16(x),
                           x_stride, in16(branch), branch_stride, alpha, in16(weight), in16(bias), rows, int(cols),
                           int(kind == ZERO_NORM_LAYER), eps, out16(res), res_stride, out16(y), y_stride, out8(codes),
                           pitch, scales, int(bpr), mean, rstd);
@@ -917,8 +897,9 @@ int zero_act_norm_backward(const void* codes, const float* scales, int format, c
     if (rows > 0) {
         const hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
             return with_shape<false>(cols, [&](auto t, auto v) {
-                return launch(norm_backward_kernel<decltype(dt)::value, decltype(fmt)::value, decltype(t)::value, decltype(v)::value>, dim3(unsigned(shape.blocks)),
-                              dim3(norm_threads<decltype(t)::value>()), s, in8(codes), pitch, scales, int(bpr), mean, rstd,
+                constexpr int D = decltype(dt)::value, M = decltype(fmt)::value, T = decltype(t)::value;
+                return launch(norm_backward_kernel<D, M, T, decltype(v)::value>, dim3(unsigned(shape.blocks)),
+                              dim3(norm_threads<T>()), s, in8(codes), pitch, scales, int(bpr), mean, rstd,
                               in16(weight), rows, shape.chunk, int(cols), int(kind == ZERO_NORM_LAYER), in16(dy),
                               dy_stride, in16(dres), dres_stride, alpha, out16(dx), dx_stride, out16(dbranch),
                               dbranch_stride, partials, int(dweight != nullptr), int(dbias != nullptr));
