@@ -61,6 +61,7 @@ struct GradArgs {
     int in_tiles, out_tiles;
     int splits;
     int64_t split_rows;  // tokens per split, a multiple of kTokens
+    int unchecked;  // the strides allow kWhole's loads
     int accumulate;
     uint16_t* dweight;
     uint16_t* dbias;
@@ -101,6 +102,8 @@ __device__ __forceinline__ s8v read_frag(const char* p) {
 }
 
 __device__ __forceinline__ constexpr int swizzle(int token) { return (token & 3) | ((token >> 1) & 4); }
+
+constexpr int kUncheckedTokens = 4 * kTokens;
 
 // How a block's tokens are loaded.  kGuarded: every load is checked against the
 // operands' edges, and what lies outside is staged as zero.  kWhole, for at least
@@ -260,16 +263,24 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, char* smem, int o0,
     }
 
     // Through LDS in fp32, 16 rows of a wave's quarter at a time, into octs of a row.
+    // Each wave has a strip of its own and LDS serves a wave in order, so within a
+    // wave only the compiler has to keep the order (the fences).  Rows are 4 floats
+    // longer than needed: the four groups of rows a write touches differ in banks.
+    constexpr int kStrip = G::kWave + 4;
+    static_assert(4 * 16 * kStrip * 4 <= 2 * G::kStageBytes, "the strips fit the stages");
     const int in8 = (g.in_cols + kOct - 1) / kOct * kOct;
-    float* strip = reinterpret_cast<float*>(smem) + wave * 16 * G::kWave;
+    float* strip = reinterpret_cast<float*>(smem) + wave * 16 * kStrip;
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < F; ++m) {
-        __syncthreads();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int n = 0; n < F; ++n)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) strip[(4 * (lane >> 4) + r) * G::kWave + 16 * n + (lane & 15)] = acc[m][n][r];
-        __syncthreads();
+            for (int r = 0; r < 4; ++r) strip[(4 * (lane >> 4) + r) * kStrip + 16 * n + (lane & 15)] = acc[m][n][r];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
         constexpr int kOctsW = G::kWave / kOct, kRows = 64 / kOctsW;
 #pragma unroll
         for (int p = 0; p < 16 / kRows; ++p) {
@@ -277,7 +288,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, char* smem, int o0,
             const int oo = o0 + (wave >> 1) * G::kWave + 16 * m + r;
             const int c = i0 + (wave & 1) * G::kWave + (lane % kOctsW) * kOct;
             if (oo >= g.out_cols || c >= g.in_cols) continue;
-            const f4* src = reinterpret_cast<const f4*>(strip + r * G::kWave + (lane % kOctsW) * kOct);
+            const f4* src = reinterpret_cast<const f4*>(strip + r * kStrip + (lane % kOctsW) * kOct);
             const f4 lo = src[0], hi = src[1];
             if (g.splits > 1) {
                 f4* dst = reinterpret_cast<f4*>(g.partials + (int64_t(split) * g.out_cols + oo) * in8 + c);
@@ -343,14 +354,15 @@ __global__ __launch_bounds__(kGradThreads) void weight_grad_kernel(GradArgs g) {
     const int o0 = ot * TILE, i0 = in * TILE;
     const int64_t t0 = split * g.split_rows;
     const int64_t t_end = t0 + g.split_rows < g.rows ? t0 + g.split_rows : g.rows;
-    const bool whole = t_end - t0 >= 4 * kTokens && g.in_cols > 0 && g.dy_stride >= kOct && g.dy_stride < (int64_t(1) << 24) &&
-                       g.pitch < (int64_t(1) << 24);
-    if (!whole)
-        grad_tile<DT, FMT, TILE, kGuarded, true>(g, smem, o0, i0, t0, t_end, split);
-    else if (g.dbias != nullptr && in == 0)
+    // TILE 256 is launched for unchecked calls in one split of at least 128 tokens only:
+    // a checked loop there would spill registers and cost every launch its scratch memory.
+    if (TILE == 128 && !(g.unchecked && t_end - t0 >= kUncheckedTokens)) {
+        if constexpr (TILE == 128) grad_tile<DT, FMT, TILE, kGuarded, true>(g, smem, o0, i0, t0, t_end, split);
+    } else if (g.dbias != nullptr && in == 0) {
         grad_tile<DT, FMT, TILE, kWhole, true>(g, smem, o0, i0, t0, t_end, split);
-    else
+    } else {
         grad_tile<DT, FMT, TILE, kWhole, false>(g, smem, o0, i0, t0, t_end, split);
+    }
 }
 
 // Adds the splits' partial gradients in split order; an oct per thread.  The
@@ -414,7 +426,10 @@ inline GradShape grad_shape(int64_t rows, int64_t in_cols, int64_t out_cols) {
         return std::max<int64_t>(1, ceil_div(in_cols, int64_t(tile))) * ceil_div(out_cols, int64_t(tile));
     };
     GradShape s;
-    s.tile = tiles(256) >= kCus ? 256 : 128;
+    // 256 x 256 tiles where they give every CU one (128 x 128 tiles take 2257 instead of 1716
+    // us for 16384 tokens, 4096 -> 16384; 256 x 256 ones 157 instead of 117 us for 4096 tokens,
+    // 1600 -> 6400) and the unchecked loop runs.
+    s.tile = rows >= kUncheckedTokens && tiles(256) >= kCus ? 256 : 128;
     s.in_tiles = int(std::max<int64_t>(1, ceil_div(in_cols, int64_t(s.tile))));
     s.out_tiles = int(ceil_div(out_cols, int64_t(s.tile)));
     const int64_t n = tiles(s.tile), steps = std::max<int64_t>(1, ceil_div(rows, int64_t(kTokens)));
@@ -491,14 +506,21 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const voi
     if (int rc = check_overlaps(fn, areas, 6)) return rc;
     if ((rows == 0 && accumulate) || (in_cols == 0 && dbias == nullptr)) return ok();
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const GradShape sh = grad_shape(rows, in_cols, out_cols);
+    GradShape sh = grad_shape(rows, in_cols, out_cols);
+    const int64_t in_pitch = sh.decode ? 2 * pitch : pitch;
+    const bool unchecked = in_cols > 0 && dy_stride >= kOct && dy_stride < (int64_t(1) << 24) && in_pitch < (int64_t(1) << 24);
+    if (sh.tile == 256 && !unchecked) {  // (one split; the workspace stays as it was sized)
+        sh.tile = 128;
+        sh.in_tiles = int(ceil_div(in_cols, int64_t(128)));
+        sh.out_tiles = int(ceil_div(out_cols, int64_t(128)));
+    }
     char* ws = static_cast<char*>(workspace);
     float* partials = reinterpret_cast<float*>(ws + decoded_bytes(sh, rows, in_cols));
     if (sh.decode)
         if (int rc = zero_act_restore(codes, scales, format, rows, in_cols, ws, pitch, dtype, stream)) return rc;
-    const GradArgs args{in16(dy), dy_stride, sh.decode ? in8(ws) : in8(codes), sh.decode ? 2 * pitch : pitch, scales,
+    const GradArgs args{in16(dy), dy_stride, sh.decode ? in8(ws) : in8(codes), in_pitch, scales,
                         int(bpr), rows, int(in_cols), int(out_cols), sh.in_tiles, sh.out_tiles, sh.splits,
-                        sh.split_rows, accumulate, out16(dweight), out16(dbias), partials,
+                        sh.split_rows, int(unchecked), accumulate, out16(dweight), out16(dbias), partials,
                         sh.splits > 1 ? partials + partial_floats(sh, in_cols, out_cols) : nullptr};
     const dim3 grid(unsigned(int64_t(sh.in_tiles) * sh.out_tiles * sh.splits));
     const auto run = [&](auto dt, auto fmt) {
