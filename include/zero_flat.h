@@ -647,7 +647,9 @@ int zero_act_norm_backward(const void* codes, const float* scales, int format, c
                            void* dbranch, int64_t dbranch_stride, int accumulate, void* dweight,
                            void* dbias, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Device workspace of zero_act_weight_grad; -1 on bad arguments. */
+/* Device workspace of zero_act_weight_grad (a 16-bit copy of the input for
+ * large products, partial sums for few outputs and many tokens, or 0); -1 on bad
+ * arguments. */
 int64_t zero_act_weight_grad_workspace_bytes(int64_t rows, int64_t in_cols, int64_t out_cols);
 
 /*

@@ -586,33 +586,45 @@ def zero_gather_dequant(plan, code_shards, scale_shards, unit_begin, unit_end, b
 # 8-bit activation checkpoints
 # ---------------------------------------------------------------------------
 
+# The checks below return the argument's address, so that each argument is looked
+# at once: a call of ten arguments costs as much as the kernels it starts.
+
 def _elsewhere(x, dev, what):
     if not x.is_cuda:
         raise ValueError(f"{what} must be a device tensor")
     raise ValueError(f"{what} is on device {x.get_device()}, the current one is {dev}")
 
 
-def _need_here(x, nbytes, dev, what):
-    """_need, and on the current device `dev` (the call's stream belongs to it)."""
-    if x is None or isinstance(x, int) or nbytes <= 0:
-        return
-    if x.get_device() != dev:
-        _elsewhere(x, dev, what)
-    _need(x, nbytes, what)
+def _flat(x, nbytes, dev, what):
+    """The address of a contiguous tensor of at least nbytes on the current device `dev` (the call's
+    stream belongs to it); None and integer addresses as they are."""
+    if x is None or isinstance(x, int):
+        return x
+    if nbytes > 0:
+        if x.get_device() != dev:
+            _elsewhere(x, dev, what)
+        if x.nbytes < nbytes or not x.is_contiguous():
+            _need(x, nbytes, what)
+    return x.data_ptr()
 
 
-def _need_matrix(x, rows, cols, stride, dev, what):
-    """A tensor argument must be a 16-bit matrix on the current device whose memory holds `rows` rows of
-    `cols` adjacent values, `stride` apart (a view into a larger matrix will do)."""
-    if x is None or isinstance(x, int) or rows <= 0 or cols <= 0:
-        return
-    if x.get_device() != dev:
-        _elsewhere(x, dev, what)
-    if x.element_size() != 2:
-        raise ValueError(f"{what} must hold 16-bit values")
-    shape, strides = x.shape, x.stride()
-    if len(shape) == 2 and strides == (stride, 1) and shape[0] >= rows and shape[1] >= cols:
-        return
+def _matrix(x, rows, cols, stride, dev, what):
+    """The address of a 16-bit matrix on the current device whose memory holds `rows` rows of `cols`
+    adjacent values, `stride` apart (a view into a larger matrix will do)."""
+    if x is None or isinstance(x, int):
+        return x
+    if rows > 0 and cols > 0:
+        if x.get_device() != dev:
+            _elsewhere(x, dev, what)
+        if x.element_size() != 2:
+            raise ValueError(f"{what} must hold 16-bit values")
+        shape, strides = x.shape, x.stride()
+        if not (len(shape) == 2 and strides == (stride, 1) and shape[0] >= rows and shape[1] >= cols):
+            _view_holds(x, shape, strides, rows, cols, stride, what)
+    return x.data_ptr()
+
+
+def _view_holds(x, shape, strides, rows, cols, stride, what):
     if len(shape) > 0 and shape[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{what}'s columns must be adjacent")
     if len(shape) == 2 and shape[0] > 1 and strides[0] != stride:
@@ -623,11 +635,13 @@ def _need_matrix(x, rows, cols, stride, dev, what):
         raise ValueError(f"{what} holds {have} values, needs {need}")
 
 
-def _need_checkpoint(codes, scales, rows, cols, dev, what=""):
-    # sizes out of range are the library's to report
-    pitch = (cols + 15) // 16 * 16
-    _need_here(codes, rows * pitch, dev, what + "codes")
-    _need_here(scales, 4 * rows * ((cols + ZERO_QBLOCK - 1) // ZERO_QBLOCK), dev, what + "scales")
+# A checkpoint's two buffers (sizes out of range are the library's to report).
+def _codes(x, rows, cols, dev, what="codes"):
+    return _flat(x, rows * ((cols + 15) // 16 * 16), dev, what)
+
+
+def _scales(x, rows, cols, dev, what="scales"):
+    return _flat(x, 4 * rows * ((cols + ZERO_QBLOCK - 1) // ZERO_QBLOCK), dev, what)
 
 
 _have_gpu = None
@@ -656,66 +670,68 @@ def zero_act_scale_count(rows, cols):
 
 
 def zero_act_save(x, x_stride, dtype, rows, cols, format, codes, scales, stream=None):
+    rows, cols = int(rows), int(cols)
+    x_stride = int(x_stride)
+    format = int(format)
     dev = _device()
-    _need_matrix(x, rows, cols, x_stride, dev, "x")
-    _need_checkpoint(codes, scales, rows, cols, dev)
-    _check(lib.zero_act_save(_ptr(x), int(x_stride), _dtype(dtype), int(rows), int(cols), int(format), _ptr(codes),
-                             _ptr(scales), _stream(stream)))
+    _check(lib.zero_act_save(_matrix(x, rows, cols, x_stride, dev, "x"), x_stride, _dtype(dtype), rows, cols, format,
+                             _codes(codes, rows, cols, dev), _scales(scales, rows, cols, dev), _stream(stream)))
 
 
 def zero_act_restore(codes, scales, format, rows, cols, y, y_stride, dtype, stream=None):
+    rows, cols = int(rows), int(cols)
+    y_stride = int(y_stride)
+    format = int(format)
     dev = _device()
-    _need_checkpoint(codes, scales, rows, cols, dev)
-    _need_matrix(y, rows, cols, y_stride, dev, "y")
-    _check(lib.zero_act_restore(_ptr(codes), _ptr(scales), int(format), int(rows), int(cols), _ptr(y), int(y_stride),
-                                _dtype(dtype), _stream(stream)))
+    _check(lib.zero_act_restore(_codes(codes, rows, cols, dev), _scales(scales, rows, cols, dev), format, rows, cols,
+                                _matrix(y, rows, cols, y_stride, dev, "y"), y_stride, _dtype(dtype),
+                                _stream(stream)))
 
 
 def zero_act_glu_forward(gate, gate_stride, up, up_stride, dtype, rows, cols, fn, format, h, h_stride, gate_codes,
                          gate_scales, up_codes, up_scales, stream=None):
+    rows, cols = int(rows), int(cols)
+    gate_stride, up_stride, h_stride = int(gate_stride), int(up_stride), int(h_stride)
+    fn, format = int(fn), int(format)
     dev = _device()
-    _need_matrix(gate, rows, cols, gate_stride, dev, "gate")
-    _need_matrix(up, rows, cols, up_stride, dev, "up")
-    _need_matrix(h, rows, cols, h_stride, dev, "h")
-    _need_checkpoint(gate_codes, gate_scales, rows, cols, dev, "gate_")
-    _need_checkpoint(up_codes, up_scales, rows, cols, dev, "up_")
-    _check(lib.zero_act_glu_forward(_ptr(gate), int(gate_stride), _ptr(up), int(up_stride), _dtype(dtype), int(rows),
-                                    int(cols), int(fn), int(format), _ptr(h), int(h_stride), _ptr(gate_codes),
-                                    _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), _stream(stream)))
+    _check(lib.zero_act_glu_forward(
+        _matrix(gate, rows, cols, gate_stride, dev, "gate"), gate_stride,
+        _matrix(up, rows, cols, up_stride, dev, "up"), up_stride, _dtype(dtype), rows, cols, fn, format,
+        _matrix(h, rows, cols, h_stride, dev, "h"), h_stride, _codes(gate_codes, rows, cols, dev, "gate_codes"),
+        _scales(gate_scales, rows, cols, dev, "gate_scales"), _codes(up_codes, rows, cols, dev, "up_codes"),
+        _scales(up_scales, rows, cols, dev, "up_scales"), _stream(stream)))
 
 
 def zero_act_glu_backward(gate_codes, gate_scales, up_codes, up_scales, format, rows, cols, fn, dh, dh_stride, dtype,
                           dgate, dgate_stride, dup, dup_stride, h=None, h_stride=0, stream=None):
+    rows, cols = int(rows), int(cols)
+    dh_stride, dgate_stride, dup_stride, h_stride = int(dh_stride), int(dgate_stride), int(dup_stride), int(h_stride)
+    format, fn = int(format), int(fn)
     dev = _device()
-    _need_checkpoint(gate_codes, gate_scales, rows, cols, dev, "gate_")
-    _need_checkpoint(up_codes, up_scales, rows, cols, dev, "up_")
-    _need_matrix(dh, rows, cols, dh_stride, dev, "dh")
-    _need_matrix(dgate, rows, cols, dgate_stride, dev, "dgate")
-    _need_matrix(dup, rows, cols, dup_stride, dev, "dup")
-    _need_matrix(h, rows, cols, h_stride, dev, "h")
-    _check(lib.zero_act_glu_backward(_ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), int(format),
-                                     int(rows), int(cols), int(fn), _ptr(dh), int(dh_stride), _dtype(dtype),
-                                     _ptr(dgate), int(dgate_stride), _ptr(dup), int(dup_stride), _ptr(h),
-                                     int(h_stride), _stream(stream)))
+    _check(lib.zero_act_glu_backward(
+        _codes(gate_codes, rows, cols, dev, "gate_codes"), _scales(gate_scales, rows, cols, dev, "gate_scales"),
+        _codes(up_codes, rows, cols, dev, "up_codes"), _scales(up_scales, rows, cols, dev, "up_scales"), format, rows,
+        cols, fn, _matrix(dh, rows, cols, dh_stride, dev, "dh"), dh_stride, _dtype(dtype),
+        _matrix(dgate, rows, cols, dgate_stride, dev, "dgate"), dgate_stride,
+        _matrix(dup, rows, cols, dup_stride, dev, "dup"), dup_stride, _matrix(h, rows, cols, h_stride, dev, "h"),
+        h_stride, _stream(stream)))
 
 
 def zero_act_norm_forward(x, x_stride, branch, branch_stride, alpha, weight, bias, dtype, rows, cols, kind, eps, format,
                           res, res_stride, y, y_stride, codes, scales, mean, rstd, stream=None):
+    rows, cols = int(rows), int(cols)
+    x_stride, branch_stride = int(x_stride), int(branch_stride)
+    res_stride, y_stride = int(res_stride), int(y_stride)
+    kind, format = int(kind), int(format)
     dev = _device()
-    _need_matrix(x, rows, cols, x_stride, dev, "x")
-    _need_matrix(branch, rows, cols, branch_stride, dev, "branch")
-    _need_matrix(res, rows, cols, res_stride, dev, "res")
-    _need_matrix(y, rows, cols, y_stride, dev, "y")
-    _need_checkpoint(codes, scales, rows, cols, dev)
-    if rows > 0:
-        _need_here(weight, 2 * cols, dev, "weight")
-        _need_here(bias, 2 * cols, dev, "bias")
-    _need_here(mean, 4 * rows, dev, "mean")
-    _need_here(rstd, 4 * rows, dev, "rstd")
-    _check(lib.zero_act_norm_forward(_ptr(x), int(x_stride), _ptr(branch), int(branch_stride), float(alpha),
-                                     _ptr(weight), _ptr(bias), _dtype(dtype), int(rows), int(cols), int(kind),
-                                     float(eps), int(format), _ptr(res), int(res_stride), _ptr(y), int(y_stride),
-                                     _ptr(codes), _ptr(scales), _ptr(mean), _ptr(rstd), _stream(stream)))
+    row = 2 * cols if rows > 0 else 0
+    _check(lib.zero_act_norm_forward(
+        _matrix(x, rows, cols, x_stride, dev, "x"), x_stride, _matrix(branch, rows, cols, branch_stride, dev, "branch"),
+        branch_stride, alpha, _flat(weight, row, dev, "weight"), _flat(bias, row, dev, "bias"), _dtype(dtype), rows,
+        cols, kind, eps, format, _matrix(res, rows, cols, res_stride, dev, "res"), res_stride,
+        _matrix(y, rows, cols, y_stride, dev, "y"), y_stride, _codes(codes, rows, cols, dev),
+        _scales(scales, rows, cols, dev), _flat(mean, 4 * rows, dev, "mean"), _flat(rstd, 4 * rows, dev, "rstd"),
+        _stream(stream)))
 
 
 def zero_act_norm_workspace_bytes(rows, cols):
@@ -728,23 +744,20 @@ def zero_act_norm_workspace_bytes(rows, cols):
 def zero_act_norm_backward(codes, scales, format, mean, rstd, weight, rows, cols, kind, dy, dy_stride, dres,
                            dres_stride, alpha, dtype, dx, dx_stride, dbranch, dbranch_stride, accumulate, dweight,
                            dbias, workspace, stream=None, workspace_bytes=None):
+    rows, cols = int(rows), int(cols)
+    dy_stride, dres_stride = int(dy_stride), int(dres_stride)
+    dx_stride, dbranch_stride = int(dx_stride), int(dbranch_stride)
+    format, kind = int(format), int(kind)
     dev = _device()
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    _need_checkpoint(codes, scales, rows, cols, dev)
-    _need_here(mean, 4 * rows, dev, "mean")
-    _need_here(rstd, 4 * rows, dev, "rstd")
-    _need_here(weight, 2 * cols, dev, "weight")
-    for t, stride, what in ((dy, dy_stride, "dy"), (dres, dres_stride, "dres"), (dx, dx_stride, "dx"),
-                            (dbranch, dbranch_stride, "dbranch")):
-        _need_matrix(t, rows, cols, stride, dev, what)
-    _need_here(dweight, 2 * cols, dev, "dweight")
-    _need_here(dbias, 2 * cols, dev, "dbias")
-    _need_here(workspace, wb, dev, "workspace")
-    _check(lib.zero_act_norm_backward(_ptr(codes), _ptr(scales), int(format), _ptr(mean), _ptr(rstd), _ptr(weight),
-                                      int(rows), int(cols), int(kind), _ptr(dy), int(dy_stride), _ptr(dres),
-                                      int(dres_stride), float(alpha), _dtype(dtype), _ptr(dx), int(dx_stride),
-                                      _ptr(dbranch), int(dbranch_stride), int(bool(accumulate)), _ptr(dweight),
-                                      _ptr(dbias), _ptr(workspace), wb, _stream(stream)))
+    _check(lib.zero_act_norm_backward(
+        _codes(codes, rows, cols, dev), _scales(scales, rows, cols, dev), format, _flat(mean, 4 * rows, dev, "mean"),
+        _flat(rstd, 4 * rows, dev, "rstd"), _flat(weight, 2 * cols, dev, "weight"), rows, cols, kind,
+        _matrix(dy, rows, cols, dy_stride, dev, "dy"), dy_stride, _matrix(dres, rows, cols, dres_stride, dev, "dres"),
+        dres_stride, alpha, _dtype(dtype), _matrix(dx, rows, cols, dx_stride, dev, "dx"), dx_stride,
+        _matrix(dbranch, rows, cols, dbranch_stride, dev, "dbranch"), dbranch_stride, bool(accumulate),
+        _flat(dweight, 2 * cols, dev, "dweight"), _flat(dbias, 2 * cols, dev, "dbias"),
+        _flat(workspace, wb, dev, "workspace"), wb, _stream(stream)))
 
 
 def zero_act_weight_grad_workspace_bytes(rows, in_cols, out_cols):
@@ -756,16 +769,16 @@ def zero_act_weight_grad_workspace_bytes(rows, in_cols, out_cols):
 
 def zero_act_weight_grad(dy, dy_stride, dtype, codes, scales, format, rows, in_cols, out_cols, accumulate, dweight,
                          dbias, workspace, stream=None, workspace_bytes=None):
+    rows, in_cols, out_cols = int(rows), int(in_cols), int(out_cols)
+    dy_stride = int(dy_stride)
+    format = int(format)
     dev = _device()
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    _need_matrix(dy, rows, out_cols, dy_stride, dev, "dy")
-    _need_checkpoint(codes, scales, rows, in_cols, dev)
-    _need_here(dweight, 2 * in_cols * out_cols, dev, "dweight")
-    _need_here(dbias, 2 * out_cols, dev, "dbias")
-    _need_here(workspace, wb, dev, "workspace")
-    _check(lib.zero_act_weight_grad(_ptr(dy), int(dy_stride), _dtype(dtype), _ptr(codes), _ptr(scales), int(format),
-                                    int(rows), int(in_cols), int(out_cols), int(bool(accumulate)), _ptr(dweight),
-                                    _ptr(dbias), _ptr(workspace), wb, _stream(stream)))
+    _check(lib.zero_act_weight_grad(
+        _matrix(dy, rows, out_cols, dy_stride, dev, "dy"), dy_stride, _dtype(dtype),
+        _codes(codes, rows, in_cols, dev), _scales(scales, rows, in_cols, dev), format, rows, in_cols, out_cols,
+        bool(accumulate), _flat(dweight, 2 * in_cols * out_cols, dev, "dweight"),
+        _flat(dbias, 2 * out_cols, dev, "dbias"), _flat(workspace, wb, dev, "workspace"), wb, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

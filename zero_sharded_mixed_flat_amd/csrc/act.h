@@ -300,7 +300,8 @@ inline bool bad_ptr(const void* p, int align) { return p == nullptr || (addr(p) 
 // The checks every entry point starts with; a negative status has been reported.
 inline int check_sizes(const char* fn, int64_t rows, int64_t cols, int dtype, int format) {
     if (!act_size_ok(rows, cols))
-        return fail(ZERO_EINVAL, std::string(fn) + ": rows, cols >= 0, cols <= 2^30 and rows * (cols rounded up to 256) <= 2^34 needed");
+        return fail(ZERO_EINVAL, std::string(fn) + ": rows and cols must be >= 0, cols <= 2^30 and rows * (cols rounded "
+                                                   "up to 256) <= 2^34");
     if (!valid_dtype(dtype)) return fail(ZERO_EINVAL, std::string(fn) + ": dtype must be ZERO_F16 or ZERO_BF16");
     if (!valid_format(format)) return fail(ZERO_EINVAL, std::string(fn) + ": format must be ZERO_ACT_INT8 or ZERO_ACT_E4M3");
     return ZERO_OK;

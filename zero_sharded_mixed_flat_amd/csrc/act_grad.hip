@@ -10,8 +10,14 @@
 // tokens are staged in LDS as they lie in memory ([token][column], 16 bits) and
 // read with the transposing LDS load (ds_read_b64_tr_b16: 16 lanes read 4 rows
 // of 16 columns and each lane receives one column of the 4 rows).  The codes are
-// decoded once per block on their way into LDS, between the matrix
-// instructions of the previous tile.
+// decoded on their way into LDS, between the matrix instructions of the previous
+// tile, or for large products beforehand, once for all blocks.
+//
+// Large products are bound by power: the matrix units are busy 58% of the cycles
+// (32 x 32 x 16 version) and the clock settles near 1.5 GHz, so what counts is
+// the energy around the products.  16384 tokens, 4096 -> 16384 in bf16: 1690 us,
+// 1300 TFLOP/s, where 16384^3 by the library reaches 1592 and the library's product
+// of this shape (both operands transposed in memory) takes 1819 us.
 
 #include "act.h"
 
@@ -169,8 +175,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, char* smem, int o0,
     const uint32_t ob = uint32_t(row) * uint32_t(g.pitch) + (i < g.in_cols ? i : 0) * kBytes;
     const uint32_t os = uint32_t(row) * uint32_t(g.blocks_per_row) * 4u;
     int loaded = 0;
-    // the next step's pass j into `set`; `last`: then on to the step after it, or past
-    // the end the last one again (staged but never used)
+    // pass j of the next step to load, into `set`
     const auto load = [&](int set, int j) {
         if constexpr (MODE == kGuarded) {
             load_checked(loaded, set, j);
@@ -178,9 +183,11 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, char* smem, int o0,
             constexpr int64_t rp = G::kRowsPerPass;
             a[set][j] = *reinterpret_cast<const u4_any*>(pa + 2 * j * rp * g.dy_stride + oa);
             b[set][j] = *reinterpret_cast<const InputOct*>(pb + j * rp * g.pitch + ob);
-            if constexpr (FMT != kDecoded) s[set][j] = *reinterpret_cast<const float*>(ps + 4 * j * rp * g.blocks_per_row + os);
+            if constexpr (FMT != kDecoded)
+                s[set][j] = *reinterpret_cast<const float*>(ps + 4 * j * rp * g.blocks_per_row + os);
         }
     };
+    // on to the step after it, or past the end the last one again (staged but never used)
     const auto advance = [&]() {
         ++loaded;
         const bool more = loaded < steps - 2;
@@ -413,6 +420,7 @@ struct GradShape {
 };
 
 constexpr int kCus = 256;
+
 // Restoring the input first costs a launch (3 us) and 3 bytes per element, and saves
 // every output tile the decoding, which draws issue slots and power from the matrix
 // units.  Measured without and with (us): 16384 tokens 4096 -> 16384 1994 / 1716;
@@ -494,7 +502,7 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const voi
         if (in_cols > 0)
             if (int rc = check_checkpoint(fn, "", codes, scales)) return rc;
         if (wb > 0 && (bad_ptr(workspace, 16) || workspace_bytes < wb))
-            return fail(ZERO_EINVAL, std::string(fn) + ": workspace NULL, not 16-byte aligned or less than zero_act_weight_grad_workspace_bytes");
+            return fail(ZERO_EINVAL, std::string(fn) + ": workspace NULL, not 16-byte aligned or too small");
     }
     const int64_t pitch = act_pitch(in_cols), bpr = act_blocks(in_cols);
     const Area areas[] = {mat16("dy", dy, rows, out_cols, dy_stride, false),
@@ -508,7 +516,8 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const voi
     hipStream_t s = static_cast<hipStream_t>(stream);
     GradShape sh = grad_shape(rows, in_cols, out_cols);
     const int64_t in_pitch = sh.decode ? 2 * pitch : pitch;
-    const bool unchecked = in_cols > 0 && dy_stride >= kOct && dy_stride < (int64_t(1) << 24) && in_pitch < (int64_t(1) << 24);
+    const int64_t far = int64_t(1) << 24;  // a pass's offsets stay within 32 bits
+    const bool unchecked = in_cols > 0 && dy_stride >= kOct && dy_stride < far && in_pitch < far;
     if (sh.tile == 256 && !unchecked) {  // (one split; the workspace stays as it was sized)
         sh.tile = 128;
         sh.in_tiles = int(ceil_div(in_cols, int64_t(128)));
@@ -528,8 +537,8 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const voi
         return sh.tile == 256 ? launch(weight_grad_kernel<D, M, 256>, grid, dim3(kGradThreads), s, args)
                               : launch(weight_grad_kernel<D, M, 128>, grid, dim3(kGradThreads), s, args);
     };
-    hipError_t e = sh.decode ? with_dtype(dtype, [&](auto dt) { return run(dt, std::integral_constant<int, kDecoded>{}); })
-                             : with_types(dtype, format, run);
+    const auto run_decoded = [&](auto dt) { return run(dt, std::integral_constant<int, kDecoded>{}); };
+    hipError_t e = sh.decode ? with_dtype(dtype, run_decoded) : with_types(dtype, format, run);
     if (e != hipSuccess || sh.splits <= 1) return hip_status(e, fn);
     const int64_t threads = ceil_div(in_cols, int64_t(kOct)) * out_cols + (dbias != nullptr ? out_cols : 0);
     e = with_dtype(dtype, [&](auto dt) {
