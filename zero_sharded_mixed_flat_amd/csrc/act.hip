@@ -543,10 +543,10 @@ __global__ __launch_bounds__(norm_threads<T>()) void norm_backward_kernel(
     }
 }
 
-// Column sums of the partials, in a fixed order: 64 threads per column take
-// every 64th partial, 8 loads in flight, then add up in a tree.  blockIdx.y is the
+// Column sums of the partials, in a fixed order: 32 threads per column take
+// every 32nd partial, 8 loads in flight, then add up in a tree.  blockIdx.y is the
 // sum: dweight's first if both are wanted.
-constexpr int kFoldCols = 16, kFoldWays = 64, kFoldThreads = kFoldCols * kFoldWays;
+constexpr int kFoldCols = 32, kFoldWays = 32, kFoldThreads = kFoldCols * kFoldWays;
 
 template <int DT>
 __global__ __launch_bounds__(kFoldThreads) void fold_columns_kernel(const float* __restrict__ partials, int count,
