@@ -25,6 +25,9 @@ owned slice of the flat parameter vector:
 * ``rounding``   -- fp32 → bf16 / fp16 round-to-nearest-even.
 * ``quant``      -- block-quantised 16-bit parameters for the gather (ZeRO++
   quantised weights; Lecture 18 notes §4.5): absmax INT8/INT4 per 256.
+* ``act``        -- 8-bit activation checkpoints and the operators that write
+  and read them (Lecture 18 notes §4.1, §4.2), with the error bounds of an fp32
+  evaluation; imported by its tests only.
 * ``step``       -- the averaged reduce-scatter slice (Lecture 18 notes §2.2
   step 3), the exact global L2 norm and clip coefficient (Lecture 18 notes
   §1.4; L3.2 §4.2 ``gradient_clipping``), the Adam(W) update of the owned
