@@ -620,8 +620,8 @@ int zero_act_norm_forward(const void* x, int64_t x_stride, const void* branch,
                           void* res, int64_t res_stride, void* y, int64_t y_stride, void* codes,
                           float* scales, float* mean, float* rstd, void* stream);
 
-/* Device workspace of zero_act_norm_backward (for the sums over rows); -1 on
- * bad arguments. */
+/* Device workspace of zero_act_norm_backward (for the sums over rows); never
+ * less for more rows.  -1 on bad arguments. */
 int64_t zero_act_norm_workspace_bytes(int64_t rows, int64_t cols);
 
 /*
@@ -648,8 +648,8 @@ int zero_act_norm_backward(const void* codes, const float* scales, int format, c
                            void* dbias, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Device workspace of zero_act_weight_grad (a 16-bit copy of the input for
- * large products, partial sums for few outputs and many tokens, or 0); -1 on bad
- * arguments. */
+ * large products, partial sums for few outputs and many tokens, or 0); never less
+ * for more rows.  -1 on bad arguments. */
 int64_t zero_act_weight_grad_workspace_bytes(int64_t rows, int64_t in_cols, int64_t out_cols);
 
 /*

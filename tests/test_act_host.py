@@ -1,6 +1,8 @@
 """Sizes and refusals of the activation-checkpoint calls (CPU: every call here
 fails in validation or has nothing to do, before the HIP runtime is touched)."""
 
+import random
+
 import pytest
 import torch
 
@@ -132,6 +134,18 @@ def test_sizes():
     with pytest.raises(abi.ZeroError):
         abi.zero_act_norm_workspace_bytes(2, 16385)
     assert abi.zero_act_norm_workspace_bytes(0, 100) == 0
+
+
+def test_a_workspace_for_more_rows_serves_fewer():
+    rng = random.Random(3)
+    for _ in range(300):
+        a, b = rng.choice([1, 40, 1024, 3000, 16384]), rng.randint(1, 20000)
+        rows = sorted(rng.randint(1, 40000) for _ in range(12)) + [4095, 4096, 4097, 5000, 127, 128, 129, 65536]
+        rows.sort()
+        norm = [abi.zero_act_norm_workspace_bytes(r, min(a, 16384)) for r in rows]
+        grad = [abi.zero_act_weight_grad_workspace_bytes(r, a, b) for r in rows]
+        assert norm == sorted(norm) and grad == sorted(grad), (a, b)
+        assert all(g % 4 == 0 for g in grad)
 
 
 def test_nothing_to_do():

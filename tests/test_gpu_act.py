@@ -184,6 +184,30 @@ def test_int8_is_the_flat_quantisers(abi):
     assert torch.equal(codes[:12 * 768], c2) and torch.equal(scales[:36], s2)
 
 
+def test_a_very_long_row_and_very_many_short_ones(abi):
+    n = 100_000_007
+    x = torch.randn(n, device="cuda").to(torch.bfloat16)
+    codes = torch.empty(abi.zero_act_code_bytes(1, n), dtype=torch.uint8, device="cuda")
+    scales = torch.empty(abi.zero_act_scale_count(1, n), device="cuda")
+    abi.zero_act_save(x, n, "bf16", 1, n, 1, codes, scales)
+    c2 = torch.empty(n, dtype=torch.uint8, device="cuda")
+    s2 = torch.empty_like(scales)
+    abi.zero_quantize_blocks(x, "bf16", n, 8, c2, s2)
+    torch.cuda.synchronize()
+    assert torch.equal(codes[:n], c2) and not codes[n:].any() and torch.equal(scales, s2)
+    rows = 3_000_001
+    codes = torch.empty(rows, 16, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(rows, device="cuda")
+    y = torch.empty(rows, dtype=torch.bfloat16, device="cuda")
+    abi.zero_act_save(x, 1, "bf16", rows, 1, 1, codes, scales)
+    abi.zero_act_restore(codes, scales, 1, rows, 1, y, 1, "bf16")
+    torch.cuda.synchronize()
+    v = x[:rows].float()
+    assert torch.equal(scales, v.abs() / torch.tensor(127.0, device="cuda"))
+    assert torch.equal(codes[:, 0].view(torch.int8).float(), 127 * torch.sign(v)) and not codes[:, 1:].any()
+    assert torch.equal(y, (127 * torch.sign(v) * scales).to(torch.bfloat16))
+
+
 def test_rows_of_a_checkpoint_are_a_checkpoint(abi):
     # A rank holding rows 20..60 of a partitioned checkpoint restores them from pointers alone.
     x = activation(np.random.default_rng(8), 64, 530, "f16")
@@ -276,7 +300,7 @@ def test_glu_at_the_ends_of_the_range(abi, fn):
         assert nan[1, :256].all() and not nan[0].any() and not nan[1, 256:].any()
 
 
-NORM_SHAPES = [(1, 16), (5, 1600), (3, 511), (9, 2049), (4, 4097), (2, 12289), (1030, 37)]
+NORM_SHAPES = [(1, 1), (3, 16384), (1, 16), (5, 1600), (3, 511), (9, 2049), (4, 4097), (2, 12289), (1030, 37)]
 
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])
@@ -372,6 +396,22 @@ def test_norm_wants_only_some_gradients(abi):
         assert np.array_equal(got[0], ref[0])
         assert np.array_equal(got[1], ref[1]) if w else (got[1] == 0x5A5A).all()
         assert np.array_equal(got[2], ref[2]) if b else (got[2] == 0x5A5A).all()
+
+
+@pytest.mark.parametrize("w,b", [(True, False), (False, True)])
+def test_norm_with_weight_or_bias_alone(abi, w, b):
+    rows, cols = 6, 777
+    rng = np.random.default_rng(4)
+    x, vec = activation(rng, rows, cols, "f16"), activation(rng, 1, cols, "f16")
+    mx, my, mv = Mat(rows, cols, "f16", x), Mat(rows, cols, "f16"), Mat(1, cols, "f16", vec, off=1)
+    codes, scales = _ckpt(abi, rows, cols)
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    abi.zero_act_norm_forward(mx.t, cols, None, 0, 0.0, mv.t if w else None, mv.t if b else None, "f16", rows, cols, 2,
+                              1e-5, 1, None, 0, my.t, cols, codes, scales, mean, rstd)
+    torch.cuda.synchronize()
+    v = wide(vec, "f16")
+    y, _, _ = act.norm_forward(wide(x, "f16"), v if w else None, v if b else None, "layer", 1e-5)
+    close16(my.bits(), *y, "f16", "y")
 
 
 def test_norm_in_place(abi):

@@ -590,6 +590,7 @@ inline int norm_row_threads(int64_t cols) { return cols <= 512 ? 64 : cols <= 20
 
 struct NormShape {
     int64_t chunk, blocks;  // the backward pass's rows per block and blocks
+    int64_t most_blocks;    // never falls as rows grow
 };
 
 // One round of blocks of 1024 threads per CU: more blocks mean more partial sums to
@@ -604,12 +605,14 @@ inline NormShape norm_shape(int64_t rows, int64_t cols) {
     NormShape s;
     s.chunk = std::max<int64_t>(1, ceil_div(passes, target)) * per_pass;
     s.blocks = ceil_div(rows, s.chunk);
+    s.most_blocks = std::min(passes, target);
     return s;
 }
 
+// Both sums' partials; a workspace for the longest batch serves all.
 inline int64_t norm_workspace(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
-    return norm_shape(rows, cols).blocks * 2 * ceil_div(cols, int64_t(kOct)) * kOct * 4;
+    return norm_shape(rows, cols).most_blocks * 2 * ceil_div(cols, int64_t(kOct)) * kOct * 4;
 }
 
 // Calls f with the row shape <T, V> for `cols`.  A thread has one oct where it can:

@@ -417,18 +417,22 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(GradArgs g) {
 
 struct GradShape {
     int tile, in_tiles, out_tiles, splits;
-    int64_t split_rows;
-    bool decode;  // restore the input first
+    int64_t split_rows, most_splits;  // the latter never falls as rows grow
+    bool decode;                      // restore the input first
 };
 
 constexpr int kCus = 256;
 
 // Restoring the input first costs a launch (3 us) and 3 bytes per element, and saves
 // every output tile the decoding, which draws issue slots and power from the matrix
-// units.  Measured without and with (us): 16384 tokens 4096 -> 16384 1994 / 1716;
-// 4096 tokens 1600 -> 6400 135 / 116; 2048 tokens 4096 -> 4096 69 / 68; 512 tokens
-// 4096 -> 4096 28 / 31; 48 tokens 1600 -> 4800 9 / 11; 16384 tokens 512 -> 512 32 / 40.
-constexpr int kDecodeTiles = 8;
+// units.  Measured without and with (us), INT8:
+//   256 x 256 tiles  16384 tokens 4096 -> 16384 1994 / 1716; 16384 tokens 16384 -> 2048
+//                    952 / 959, -> 1024 523 / 566; 2048 tokens 4096 -> 4096 69 / 68;
+//                    512 tokens 4096 -> 4096 28 / 31
+//   128 x 128 tiles  4096 tokens 1600 -> 6400 135 / 116, 6400 -> 1600 135 / 127; 16384
+//                    tokens 2048 -> 1024 97 / 113; 48 tokens 1600 -> 4800 9 / 11
+constexpr int64_t kDecodeOutputs = 1536;       // with 128 x 128 tiles
+constexpr int64_t kDecodeOutputsLarge = 2048;  // with 256 x 256 tiles, which decode half as often
 constexpr int64_t kDecodeProducts = 10000000000;
 
 inline GradShape grad_shape(int64_t rows, int64_t in_cols, int64_t out_cols) {
@@ -444,10 +448,11 @@ inline GradShape grad_shape(int64_t rows, int64_t in_cols, int64_t out_cols) {
     s.out_tiles = int(ceil_div(out_cols, int64_t(s.tile)));
     const int64_t n = tiles(s.tile), steps = std::max<int64_t>(1, ceil_div(rows, int64_t(kTokens)));
     // few tiles and many tokens: enough splits for two blocks per CU, of at least 16 staged tiles each
-    int64_t want = n >= kCus ? 1 : std::min(ceil_div(2 * kCus, n), std::max<int64_t>(1, steps / 16));
-    s.split_rows = ceil_div(steps, want) * kTokens;
+    s.most_splits = n >= kCus ? 1 : std::min(ceil_div(2 * kCus, n), std::max<int64_t>(1, steps / 16));
+    s.split_rows = ceil_div(steps, s.most_splits) * kTokens;
     s.splits = int(std::max<int64_t>(1, ceil_div(rows, s.split_rows)));
-    s.decode = s.out_tiles >= kDecodeTiles && rows > 0 && in_cols * out_cols >= kDecodeProducts / rows;
+    const int64_t outputs = tiles(256) >= kCus ? kDecodeOutputsLarge : kDecodeOutputs;
+    s.decode = out_cols >= outputs && rows > 0 && in_cols * out_cols >= kDecodeProducts / rows;
     return s;
 }
 
@@ -464,12 +469,13 @@ inline int64_t decoded_bytes(const GradShape& s, int64_t rows, int64_t in_cols) 
     return s.decode ? 2 * rows * act_pitch(in_cols) : 0;
 }
 
-// The restored input, if there is one, then the partial gradients.
+// The restored input, if there is one, then the partial gradients.  Sized by what
+// never falls as rows grow, so that a workspace for the longest batch serves all.
 inline int64_t weight_grad_workspace(int64_t rows, int64_t in_cols, int64_t out_cols) {
     if (rows == 0 || out_cols == 0) return 0;
     const GradShape s = grad_shape(rows, in_cols, out_cols);
-    return decoded_bytes(s, rows, in_cols) +
-           (s.splits > 1 ? 4 * (partial_floats(s, in_cols, out_cols) + s.splits * out_cols) : 0);
+    const int64_t in8 = ceil_div(in_cols, int64_t(kOct)) * kOct;
+    return decoded_bytes(s, rows, in_cols) + (s.most_splits > 1 ? 4 * s.most_splits * out_cols * (in8 + 1) : 0);
 }
 
 }  // namespace
