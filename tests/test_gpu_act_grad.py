@@ -93,6 +93,7 @@ def test_integers_are_exact(abi):
     (4801, 1030, 2056),    # 128 x 128 tiles, restored first, split over the tokens
     (130, 520, 70_000),    # one row of input tiles
     (40_000, 120, 9),      # one tile, many splits, fewer than a quarter of it used
+    (130, 70_000, 5),      # large enough for 256 x 256 tiles, rows too close for their loads
 ])
 def test_large_shapes_are_exact(abi, dtype, fmt, rows, inner, outer):
     # Integers as above (E4M3 holds those up to 16 with a block maximum of 448), checked in fp64 on the GPU.
@@ -195,6 +196,12 @@ def test_no_rows_no_columns(abi):
         torch.cuda.synchronize()
         assert (wide(b.bits(), "bf16") == rows).all()
     abi.zero_act_weight_grad(0, 0, "bf16", 0, 0, 1, 9, 7, 0, False, 0, None, None, workspace_bytes=0)
+    many = Mat(130, 70_001, "bf16", np.full((130, 70_001), 0x3F80, np.uint16))
+    b = Mat(1, 70_001, "bf16")
+    abi.zero_act_weight_grad(many.t, 70_001, "bf16", 0, 0, 1, 130, 0, 70_001, False, 0, b.view.view(-1), None,
+                             workspace_bytes=0)
+    torch.cuda.synchronize()
+    assert (wide(b.bits(), "bf16") == 130).all() and b.guards_intact()
 
 
 def test_repeatable_and_independent_of_the_workspaces_content(abi):

@@ -391,10 +391,10 @@ __global__ __launch_bounds__(norm_threads<T>()) void norm_forward_kernel(
 }
 
 // Block b does rows [b chunk, (b + 1) chunk), loading each row while the one
-// before is computed (rows of up to 8192 columns); its threads keep the column sums of dy n and dy for their
-// columns over all of them, and write the wanted ones to the workspace as partial
-// b: [blocks][sums][cols8] fp32 (cols8: cols rounded up to an oct), added up by
-// fold_columns_kernel.
+// before is computed (rows of up to 8192 columns).  Its threads keep the column
+// sums of dy n and dy for their columns over all of them, and write the wanted ones
+// to the workspace as partial b: [blocks][sums][cols8] fp32 (cols8: cols rounded up
+// to an oct), added up by fold_columns_kernel.
 template <int DT, int FMT, int T, int V>
 __global__ __launch_bounds__(norm_threads<T>()) void norm_backward_kernel(
     const uint8_t* __restrict__ codes, int64_t pitch, const float* __restrict__ scales, int blocks_per_row,

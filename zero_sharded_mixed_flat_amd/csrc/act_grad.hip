@@ -528,7 +528,7 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const voi
     const bool unchecked = in_cols > 0 && dy_stride >= kOct && dy_stride < far && in_pitch < far;
     if (sh.tile == 256 && !unchecked) {  // (one split; the workspace stays as it was sized)
         sh.tile = 128;
-        sh.in_tiles = int(ceil_div(in_cols, int64_t(128)));
+        sh.in_tiles = int(std::max<int64_t>(1, ceil_div(in_cols, int64_t(128))));
         sh.out_tiles = int(ceil_div(out_cols, int64_t(128)));
     }
     char* ws = static_cast<char*>(workspace);
