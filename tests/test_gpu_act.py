@@ -484,6 +484,30 @@ def test_empty_calls(abi):
         g.t.fill_(1.0)
 
 
+@pytest.mark.parametrize("rows,cols", [(2_097_160, 520), (8_388_613, 24)])
+def test_norm_of_more_rows_than_one_launch(abi, rows, cols):
+    # 2^21 blocks are a launch; the rows around the seam and the last ones equal the same rows alone.
+    x = torch.randn(rows, cols, device="cuda").to(torch.bfloat16)
+    br = torch.randn(cols, device="cuda").to(torch.bfloat16).expand(rows, cols).contiguous()
+
+    def run(sl):
+        xs, bs = x[sl].clone(), br[sl].contiguous()
+        n = xs.shape[0]
+        y, (codes, scales) = torch.empty_like(xs), _ckpt(abi, n, cols)
+        mean, rstd = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        abi.zero_act_norm_forward(xs, cols, bs, cols, 1.0, None, None, "bf16", n, cols, 2, 1e-5, 1, xs, cols, y, cols,
+                                  codes, scales, mean, rstd)
+        torch.cuda.synchronize()
+        return (xs, y, codes[:n * ((cols + 15) // 16 * 16)].view(n, -1), scales[:n * -(-cols // 256)].view(n, -1), mean,
+                rstd)
+
+    whole = run(slice(0, rows))
+    seam = (1 << 21) * (1 if cols > 512 else 4)
+    for sl in (slice(seam - 6, min(seam + 6, rows)), slice(rows - 3, rows), slice(0, 5)):
+        for a, b in zip(whole, run(sl)):
+            assert torch.equal(a[sl], b)
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_offsets_past_32_bits(abi, fmt):
     # 2.2e9 elements, 4.4 GB of 16-bit values, 2.2 GB of codes: the last rows equal the same rows saved alone.

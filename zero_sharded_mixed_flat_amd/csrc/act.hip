@@ -835,11 +835,20 @@ int zero_act_norm_forward(const void* x, int64_t x_stride, const void* branch, i
     const hipError_t e = with_types(dtype, format, [&](auto dt, auto fmt) {
         return with_shape<true>(cols, [&](auto t, auto v) {
             constexpr int D = decltype(dt)::value, M = decltype(fmt)::value, T = decltype(t)::value;
-            const dim3 grid{unsigned(ceil_div(rows, int64_t(norm_rows<T>())))};
-            return launch(norm_forward_kernel<D, M, T, decltype(v)::value>, grid, dim3(norm_threads<T>()), s, in16(x),
-                          x_stride, in16(branch), branch_stride, alpha, in16(weight), in16(bias), rows, int(cols),
-                          int(kind == ZERO_NORM_LAYER), eps, out16(res), res_stride, out16(y), y_stride, out8(codes),
-                          pitch, scales, int(bpr), mean, rstd);
+            // A launch's work-items are counted in 32 bits: 2^21 blocks of at most 1024 at a time.
+            constexpr int64_t kSlice = (int64_t(1) << 21) * norm_rows<T>();
+            for (int64_t r = 0; r < rows; r += kSlice) {
+                const int64_t n = std::min(kSlice, rows - r);
+                const dim3 grid{unsigned(ceil_div(n, int64_t(norm_rows<T>())))};
+                const hipError_t err = launch(
+                    norm_forward_kernel<D, M, T, decltype(v)::value>, grid, dim3(norm_threads<T>()), s,
+                    in16(x) + r * x_stride, x_stride, branch ? in16(branch) + r * branch_stride : nullptr, branch_stride,
+                    alpha, in16(weight), in16(bias), n, int(cols), int(kind == ZERO_NORM_LAYER), eps,
+                    res ? out16(res) + r * res_stride : nullptr, res_stride, out16(y) + r * y_stride, y_stride,
+                    out8(codes) + r * pitch, pitch, scales + r * bpr, int(bpr), mean ? mean + r : nullptr, rstd + r);
+                if (err != hipSuccess) return err;
+            }
+            return hipSuccess;
         });
     });
     return hip_status(e, fn);
