@@ -536,7 +536,9 @@ int zero_gather_dequant(const zero_plan* plan, const void* const* code_shards,
  * outputs may not overlap each other or an input (ZERO_EALIAS), except where a
  * call says so.  `dtype` is that of every 16-bit array of the call.
  * 0 <= rows, 0 <= cols <= ZERO_ACT_MAX_COLS, and rows * (cols rounded up to
- * ZERO_QBLOCK) <= ZERO_MAX_ELEMS.  Sums are fp32 in an order that depends only on the sizes,
+ * ZERO_QBLOCK) <= ZERO_MAX_ELEMS.  With no rows or no columns the arrays that
+ * then hold nothing may be NULL or not, also where a call says which go
+ * together.  Sums are fp32 in an order that depends only on the sizes,
  * so results are bitwise repeatable.  Nothing is allocated, copied to the
  * host or recorded as a memset: every call can be captured in a HIP graph.
  */

@@ -715,10 +715,10 @@ int zero_act_glu_forward(const void* gate, int64_t gate_stride, const void* up, 
     if (int rc = check_sizes(fn, rows, cols, dtype, format)) return rc;
     if (fn_id < ZERO_GLU_SILU || fn_id > ZERO_GLU_GELU_TANH)
         return fail(ZERO_EINVAL, std::string(fn) + ": fn must be ZERO_GLU_SILU, ZERO_GLU_GELU or ZERO_GLU_GELU_TANH");
+    if (rows == 0 || cols == 0) return ok();  // arrays without elements may be NULL, whatever they stand for
     const bool gated = up != nullptr;
     if (!gated && (up_codes != nullptr || up_scales != nullptr))
         return fail(ZERO_EINVAL, std::string(fn) + ": up_codes and up_scales must be NULL when up is");
-    if (rows == 0 || cols == 0) return ok();
     if (int rc = check_matrix(fn, "gate", gate, rows, cols, gate_stride)) return rc;
     if (int rc = check_matrix(fn, "h", h, rows, cols, h_stride)) return rc;
     if (int rc = check_checkpoint(fn, "gate_", gate_codes, gate_scales)) return rc;
@@ -756,10 +756,10 @@ int zero_act_glu_backward(const void* gate_codes, const float* gate_scales, cons
     if (int rc = check_sizes(fn, rows, cols, dtype, format)) return rc;
     if (fn_id < ZERO_GLU_SILU || fn_id > ZERO_GLU_GELU_TANH)
         return fail(ZERO_EINVAL, std::string(fn) + ": fn must be ZERO_GLU_SILU, ZERO_GLU_GELU or ZERO_GLU_GELU_TANH");
+    if (rows == 0 || cols == 0) return ok();  // arrays without elements may be NULL, whatever they stand for
     const bool gated = up_codes != nullptr;
     if ((up_scales != nullptr) != gated || (dup != nullptr) != gated)
         return fail(ZERO_EINVAL, std::string(fn) + ": up_codes, up_scales and dup are given together or all NULL");
-    if (rows == 0 || cols == 0) return ok();
     if (int rc = check_checkpoint(fn, "gate_", gate_codes, gate_scales)) return rc;
     if (int rc = check_matrix(fn, "dh", dh, rows, cols, dh_stride)) return rc;
     if (int rc = check_matrix(fn, "dgate", dgate, rows, cols, dgate_stride)) return rc;
@@ -802,12 +802,12 @@ int zero_act_norm_forward(const void* x, int64_t x_stride, const void* branch, i
     if (kind != ZERO_NORM_RMS && kind != ZERO_NORM_LAYER)
         return fail(ZERO_EINVAL, std::string(fn) + ": kind must be ZERO_NORM_RMS or ZERO_NORM_LAYER");
     if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(ZERO_EINVAL, std::string(fn) + ": eps must be positive and finite");
+    if (branch != nullptr && !std::isfinite(alpha)) return fail(ZERO_EINVAL, std::string(fn) + ": alpha must be finite");
+    if (rows == 0 || cols == 0) return ok();  // arrays without elements may be NULL, whatever they stand for
     if ((branch != nullptr) != (res != nullptr))
         return fail(ZERO_EINVAL, std::string(fn) + ": branch and res are given together or both NULL");
-    if (branch != nullptr && !std::isfinite(alpha)) return fail(ZERO_EINVAL, std::string(fn) + ": alpha must be finite");
     if ((kind == ZERO_NORM_RMS) != (mean == nullptr))
         return fail(ZERO_EINVAL, std::string(fn) + ": mean is given for ZERO_NORM_LAYER and NULL for ZERO_NORM_RMS");
-    if (rows == 0 || cols == 0) return ok();
     if (int rc = check_matrix(fn, "x", x, rows, cols, x_stride)) return rc;
     if (branch != nullptr) {
         if (int rc = check_matrix(fn, "branch", branch, rows, cols, branch_stride)) return rc;
@@ -874,8 +874,6 @@ int zero_act_norm_backward(const void* codes, const float* scales, int format, c
     if (kind != ZERO_NORM_RMS && kind != ZERO_NORM_LAYER)
         return fail(ZERO_EINVAL, std::string(fn) + ": kind must be ZERO_NORM_RMS or ZERO_NORM_LAYER");
     if (dbranch != nullptr && !std::isfinite(alpha)) return fail(ZERO_EINVAL, std::string(fn) + ": alpha must be finite");
-    if ((kind == ZERO_NORM_RMS) != (mean == nullptr))
-        return fail(ZERO_EINVAL, std::string(fn) + ": mean is given for ZERO_NORM_LAYER and NULL for ZERO_NORM_RMS");
     if ((dweight != nullptr && (addr(dweight) & 1)) || (dbias != nullptr && (addr(dbias) & 1)) ||
         (weight != nullptr && (addr(weight) & 1)))
         return fail(ZERO_EINVAL, std::string(fn) + ": weight, dweight or dbias not 2-byte aligned");
@@ -883,6 +881,8 @@ int zero_act_norm_backward(const void* codes, const float* scales, int format, c
     const bool sums = dweight != nullptr || dbias != nullptr;
     const int64_t pitch = act_pitch(cols), bpr = act_blocks(cols), wb = sums ? norm_workspace(rows, cols) : 0;
     if (rows > 0) {
+        if ((kind == ZERO_NORM_RMS) != (mean == nullptr))
+            return fail(ZERO_EINVAL, std::string(fn) + ": mean is given for ZERO_NORM_LAYER and NULL for ZERO_NORM_RMS");
         if (int rc = check_checkpoint(fn, "", codes, scales)) return rc;
         if (int rc = check_matrix(fn, "dy", dy, rows, cols, dy_stride)) return rc;
         if (dres != nullptr)
