@@ -609,8 +609,9 @@ def _flat(x, nbytes, dev, what):
 
 
 def _matrix(x, rows, cols, stride, dev, what):
-    """The address of a 16-bit matrix on the current device whose memory holds `rows` rows of `cols`
-    adjacent values, `stride` apart (a view into a larger matrix will do)."""
+    """The address of a 16-bit matrix on the current device: a view whose rows, `stride` apart, hold `rows`
+    rows of `cols` adjacent values (more dimensions than two if they lie in memory as such rows do), or
+    contiguous memory of that extent."""
     if x is None or isinstance(x, int):
         return x
     if rows > 0 and cols > 0:
@@ -620,19 +621,40 @@ def _matrix(x, rows, cols, stride, dev, what):
             raise ValueError(f"{what} must hold 16-bit values")
         shape, strides = x.shape, x.stride()
         if not (len(shape) == 2 and strides == (stride, 1) and shape[0] >= rows and shape[1] >= cols):
-            _view_holds(x, shape, strides, rows, cols, stride, what)
+            _view_holds(shape, strides, rows, cols, stride, what)
     return x.data_ptr()
 
 
-def _view_holds(x, shape, strides, rows, cols, stride, what):
+def _view_holds(shape, strides, rows, cols, stride, what):
     if len(shape) > 0 and shape[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{what}'s columns must be adjacent")
     if len(shape) == 2 and shape[0] > 1 and strides[0] != stride:
         raise ValueError(f"{what}'s rows are {strides[0]} apart, not {stride}")
-    have = x.untyped_storage().nbytes() // 2 - x.storage_offset()
-    need = (rows - 1) * stride + cols
-    if have < need:
-        raise ValueError(f"{what} holds {have} values, needs {need}")
+    # The fewest (size, stride) pairs that visit the same memory in the same order.
+    dims = []
+    for size, step in zip(reversed(shape), reversed(strides)):
+        if size == 0:
+            raise ValueError(f"{what} holds no values")
+        if size == 1:
+            continue
+        if dims and step == dims[-1][0] * dims[-1][1]:
+            dims[-1] = (size * dims[-1][0], dims[-1][1])
+        else:
+            dims.append((size, step))
+    if not dims or dims[0][1] != 1:
+        dims.insert(0, (1, 1))            # a single column
+    if len(dims) == 1:
+        have, need = dims[0][0], (rows - 1) * stride + cols
+        if have < need:
+            raise ValueError(f"{what} holds {have} values, needs {need}")
+        return
+    if len(dims) > 2:
+        raise ValueError(f"{what}'s rows are not evenly apart")
+    (have_cols, _), (have_rows, step) = dims
+    if step != stride:
+        raise ValueError(f"{what}'s rows are {step} apart, not {stride}")
+    if have_rows < rows or have_cols < cols:
+        raise ValueError(f"{what} holds {have_rows} rows of {have_cols} values, needs {rows} of {cols}")
 
 
 # A checkpoint's two buffers (sizes out of range are the library's to report).
