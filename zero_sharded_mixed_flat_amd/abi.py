@@ -254,11 +254,12 @@ def _dtype(d):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
+    """The stream's handle; None is the current stream (of the current device, `dev` if the caller has it)."""
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if dev is None else dev)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -595,33 +596,48 @@ def _elsewhere(x, dev, what):
     raise ValueError(f"{what} is on device {x.get_device()}, the current one is {dev}")
 
 
-def _flat(x, nbytes, dev, what):
-    """The address of a contiguous tensor of at least nbytes on the current device `dev` (the call's
-    stream belongs to it); None and integer addresses as they are."""
+# What a call's dtype is in torch (the library reports any other).
+_HALF = {ZERO_F16: torch.float16, ZERO_BF16: torch.bfloat16}
+
+
+def _other_type(x, want, what):
+    """A floating tensor of another type than `want` holds other values; integer types are taken as the
+    patterns that the call describes."""
+    if want is not None and (x.is_floating_point() or x.is_complex()):
+        raise ValueError(f"{what} holds {x.dtype} values, not {want}")
+
+
+def _flat(x, nbytes, dev, what, want=None):
+    """The address of a contiguous tensor of at least nbytes of type `want` on the current device `dev`
+    (the call's stream belongs to it); None and integer addresses as they are."""
     if x is None or isinstance(x, int):
         return x
     if nbytes > 0:
         if x.get_device() != dev:
             _elsewhere(x, dev, what)
+        if want is not None and x.dtype is not want:
+            _other_type(x, want, what)
         if x.nbytes < nbytes or not x.is_contiguous():
             _need(x, nbytes, what)
     return x.data_ptr()
 
 
-def _matrix(x, rows, cols, stride, dev, what):
-    """The address of a 16-bit matrix on the current device: a view whose rows, `stride` apart, hold `rows`
-    rows of `cols` adjacent values (more dimensions than two if they lie in memory as such rows do), or
-    contiguous memory of that extent."""
+def _matrix(x, rows, cols, stride, dev, what, want=None):
+    """The address of a 16-bit matrix (of type `want`) on the current device: a view whose rows, `stride` apart,
+    hold `rows` rows of `cols` adjacent values (more dimensions than two if they lie in memory as such rows do),
+    or contiguous memory of that extent."""
     if x is None or isinstance(x, int):
         return x
     if rows > 0 and cols > 0:
         if x.get_device() != dev:
             _elsewhere(x, dev, what)
-        if x.element_size() != 2:
-            raise ValueError(f"{what} must hold 16-bit values")
         shape, strides = x.shape, x.stride()
         if not (len(shape) == 2 and strides == (stride, 1) and shape[0] >= rows and shape[1] >= cols):
             _view_holds(shape, strides, rows, cols, stride, what)
+        if getattr(x, "dtype", None) is not want or want is None:
+            if x.element_size() != 2:
+                raise ValueError(f"{what} must hold 16-bit values")
+            _other_type(x, want, what)
     return x.data_ptr()
 
 
@@ -663,7 +679,7 @@ def _codes(x, rows, cols, dev, what="codes"):
 
 
 def _scales(x, rows, cols, dev, what="scales"):
-    return _flat(x, 4 * rows * ((cols + ZERO_QBLOCK - 1) // ZERO_QBLOCK), dev, what)
+    return _flat(x, 4 * rows * ((cols + ZERO_QBLOCK - 1) // ZERO_QBLOCK), dev, what, torch.float32)
 
 
 _have_gpu = None
@@ -695,19 +711,21 @@ def zero_act_save(x, x_stride, dtype, rows, cols, format, codes, scales, stream=
     rows, cols = int(rows), int(cols)
     x_stride = int(x_stride)
     format = int(format)
-    dev = _device()
-    _check(lib.zero_act_save(_matrix(x, rows, cols, x_stride, dev, "x"), x_stride, _dtype(dtype), rows, cols, format,
-                             _codes(codes, rows, cols, dev), _scales(scales, rows, cols, dev), _stream(stream)))
+    dev, dt = _device(), _dtype(dtype)
+    want = _HALF.get(dt)
+    _check(lib.zero_act_save(_matrix(x, rows, cols, x_stride, dev, "x", want), x_stride, dt, rows, cols, format,
+                             _codes(codes, rows, cols, dev), _scales(scales, rows, cols, dev), _stream(stream, dev)))
 
 
 def zero_act_restore(codes, scales, format, rows, cols, y, y_stride, dtype, stream=None):
     rows, cols = int(rows), int(cols)
     y_stride = int(y_stride)
     format = int(format)
-    dev = _device()
+    dev, dt = _device(), _dtype(dtype)
+    want = _HALF.get(dt)
     _check(lib.zero_act_restore(_codes(codes, rows, cols, dev), _scales(scales, rows, cols, dev), format, rows, cols,
-                                _matrix(y, rows, cols, y_stride, dev, "y"), y_stride, _dtype(dtype),
-                                _stream(stream)))
+                                _matrix(y, rows, cols, y_stride, dev, "y", want), y_stride, dt,
+                                _stream(stream, dev)))
 
 
 def zero_act_glu_forward(gate, gate_stride, up, up_stride, dtype, rows, cols, fn, format, h, h_stride, gate_codes,
@@ -715,13 +733,14 @@ def zero_act_glu_forward(gate, gate_stride, up, up_stride, dtype, rows, cols, fn
     rows, cols = int(rows), int(cols)
     gate_stride, up_stride, h_stride = int(gate_stride), int(up_stride), int(h_stride)
     fn, format = int(fn), int(format)
-    dev = _device()
+    dev, dt = _device(), _dtype(dtype)
+    want = _HALF.get(dt)
     _check(lib.zero_act_glu_forward(
-        _matrix(gate, rows, cols, gate_stride, dev, "gate"), gate_stride,
-        _matrix(up, rows, cols, up_stride, dev, "up"), up_stride, _dtype(dtype), rows, cols, fn, format,
-        _matrix(h, rows, cols, h_stride, dev, "h"), h_stride, _codes(gate_codes, rows, cols, dev, "gate_codes"),
+        _matrix(gate, rows, cols, gate_stride, dev, "gate", want), gate_stride,
+        _matrix(up, rows, cols, up_stride, dev, "up", want), up_stride, dt, rows, cols, fn, format,
+        _matrix(h, rows, cols, h_stride, dev, "h", want), h_stride, _codes(gate_codes, rows, cols, dev, "gate_codes"),
         _scales(gate_scales, rows, cols, dev, "gate_scales"), _codes(up_codes, rows, cols, dev, "up_codes"),
-        _scales(up_scales, rows, cols, dev, "up_scales"), _stream(stream)))
+        _scales(up_scales, rows, cols, dev, "up_scales"), _stream(stream, dev)))
 
 
 def zero_act_glu_backward(gate_codes, gate_scales, up_codes, up_scales, format, rows, cols, fn, dh, dh_stride, dtype,
@@ -729,14 +748,15 @@ def zero_act_glu_backward(gate_codes, gate_scales, up_codes, up_scales, format, 
     rows, cols = int(rows), int(cols)
     dh_stride, dgate_stride, dup_stride, h_stride = int(dh_stride), int(dgate_stride), int(dup_stride), int(h_stride)
     format, fn = int(format), int(fn)
-    dev = _device()
+    dev, dt = _device(), _dtype(dtype)
+    want = _HALF.get(dt)
     _check(lib.zero_act_glu_backward(
         _codes(gate_codes, rows, cols, dev, "gate_codes"), _scales(gate_scales, rows, cols, dev, "gate_scales"),
         _codes(up_codes, rows, cols, dev, "up_codes"), _scales(up_scales, rows, cols, dev, "up_scales"), format, rows,
-        cols, fn, _matrix(dh, rows, cols, dh_stride, dev, "dh"), dh_stride, _dtype(dtype),
-        _matrix(dgate, rows, cols, dgate_stride, dev, "dgate"), dgate_stride,
-        _matrix(dup, rows, cols, dup_stride, dev, "dup"), dup_stride, _matrix(h, rows, cols, h_stride, dev, "h"),
-        h_stride, _stream(stream)))
+        cols, fn, _matrix(dh, rows, cols, dh_stride, dev, "dh", want), dh_stride, dt,
+        _matrix(dgate, rows, cols, dgate_stride, dev, "dgate", want), dgate_stride,
+        _matrix(dup, rows, cols, dup_stride, dev, "dup", want), dup_stride,
+        _matrix(h, rows, cols, h_stride, dev, "h", want), h_stride, _stream(stream, dev)))
 
 
 def zero_act_norm_forward(x, x_stride, branch, branch_stride, alpha, weight, bias, dtype, rows, cols, kind, eps, format,
@@ -745,15 +765,17 @@ def zero_act_norm_forward(x, x_stride, branch, branch_stride, alpha, weight, bia
     x_stride, branch_stride = int(x_stride), int(branch_stride)
     res_stride, y_stride = int(res_stride), int(y_stride)
     kind, format = int(kind), int(format)
-    dev = _device()
+    dev, dt = _device(), _dtype(dtype)
+    want = _HALF.get(dt)
     row = 2 * cols if rows > 0 else 0
     _check(lib.zero_act_norm_forward(
-        _matrix(x, rows, cols, x_stride, dev, "x"), x_stride, _matrix(branch, rows, cols, branch_stride, dev, "branch"),
-        branch_stride, alpha, _flat(weight, row, dev, "weight"), _flat(bias, row, dev, "bias"), _dtype(dtype), rows,
-        cols, kind, eps, format, _matrix(res, rows, cols, res_stride, dev, "res"), res_stride,
-        _matrix(y, rows, cols, y_stride, dev, "y"), y_stride, _codes(codes, rows, cols, dev),
-        _scales(scales, rows, cols, dev), _flat(mean, 4 * rows, dev, "mean"), _flat(rstd, 4 * rows, dev, "rstd"),
-        _stream(stream)))
+        _matrix(x, rows, cols, x_stride, dev, "x", want), x_stride,
+        _matrix(branch, rows, cols, branch_stride, dev, "branch", want), branch_stride, alpha,
+        _flat(weight, row, dev, "weight", want), _flat(bias, row, dev, "bias", want), dt, rows, cols, kind, eps, format,
+        _matrix(res, rows, cols, res_stride, dev, "res", want), res_stride,
+        _matrix(y, rows, cols, y_stride, dev, "y", want), y_stride, _codes(codes, rows, cols, dev),
+        _scales(scales, rows, cols, dev), _flat(mean, 4 * rows, dev, "mean", torch.float32),
+        _flat(rstd, 4 * rows, dev, "rstd", torch.float32), _stream(stream, dev)))
 
 
 def zero_act_norm_workspace_bytes(rows, cols):
@@ -770,16 +792,19 @@ def zero_act_norm_backward(codes, scales, format, mean, rstd, weight, rows, cols
     dy_stride, dres_stride = int(dy_stride), int(dres_stride)
     dx_stride, dbranch_stride = int(dx_stride), int(dbranch_stride)
     format, kind = int(format), int(kind)
-    dev = _device()
+    dev, dt = _device(), _dtype(dtype)
+    want = _HALF.get(dt)
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
     _check(lib.zero_act_norm_backward(
-        _codes(codes, rows, cols, dev), _scales(scales, rows, cols, dev), format, _flat(mean, 4 * rows, dev, "mean"),
-        _flat(rstd, 4 * rows, dev, "rstd"), _flat(weight, 2 * cols, dev, "weight"), rows, cols, kind,
-        _matrix(dy, rows, cols, dy_stride, dev, "dy"), dy_stride, _matrix(dres, rows, cols, dres_stride, dev, "dres"),
-        dres_stride, alpha, _dtype(dtype), _matrix(dx, rows, cols, dx_stride, dev, "dx"), dx_stride,
-        _matrix(dbranch, rows, cols, dbranch_stride, dev, "dbranch"), dbranch_stride, bool(accumulate),
-        _flat(dweight, 2 * cols, dev, "dweight"), _flat(dbias, 2 * cols, dev, "dbias"),
-        _flat(workspace, wb, dev, "workspace"), wb, _stream(stream)))
+        _codes(codes, rows, cols, dev), _scales(scales, rows, cols, dev), format,
+        _flat(mean, 4 * rows, dev, "mean", torch.float32), _flat(rstd, 4 * rows, dev, "rstd", torch.float32),
+        _flat(weight, 2 * cols, dev, "weight", want), rows, cols, kind,
+        _matrix(dy, rows, cols, dy_stride, dev, "dy", want), dy_stride,
+        _matrix(dres, rows, cols, dres_stride, dev, "dres", want), dres_stride, alpha, dt,
+        _matrix(dx, rows, cols, dx_stride, dev, "dx", want), dx_stride,
+        _matrix(dbranch, rows, cols, dbranch_stride, dev, "dbranch", want), dbranch_stride, bool(accumulate),
+        _flat(dweight, 2 * cols, dev, "dweight", want), _flat(dbias, 2 * cols, dev, "dbias", want),
+        _flat(workspace, wb, dev, "workspace"), wb, _stream(stream, dev)))
 
 
 def zero_act_weight_grad_workspace_bytes(rows, in_cols, out_cols):
@@ -794,13 +819,15 @@ def zero_act_weight_grad(dy, dy_stride, dtype, codes, scales, format, rows, in_c
     rows, in_cols, out_cols = int(rows), int(in_cols), int(out_cols)
     dy_stride = int(dy_stride)
     format = int(format)
-    dev = _device()
+    dev, dt = _device(), _dtype(dtype)
+    want = _HALF.get(dt)
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
     _check(lib.zero_act_weight_grad(
-        _matrix(dy, rows, out_cols, dy_stride, dev, "dy"), dy_stride, _dtype(dtype),
+        _matrix(dy, rows, out_cols, dy_stride, dev, "dy", want), dy_stride, dt,
         _codes(codes, rows, in_cols, dev), _scales(scales, rows, in_cols, dev), format, rows, in_cols, out_cols,
-        bool(accumulate), _flat(dweight, 2 * in_cols * out_cols, dev, "dweight"),
-        _flat(dbias, 2 * out_cols, dev, "dbias"), _flat(workspace, wb, dev, "workspace"), wb, _stream(stream)))
+        bool(accumulate), _flat(dweight, 2 * in_cols * out_cols, dev, "dweight", want),
+        _flat(dbias, 2 * out_cols, dev, "dbias", want), _flat(workspace, wb, dev, "workspace"), wb,
+        _stream(stream, dev)))
 
 
 # ---------------------------------------------------------------------------
