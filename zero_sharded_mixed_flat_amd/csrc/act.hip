@@ -118,16 +118,21 @@ __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(
 //
 // SiLU and tanh-GELU are g s(z) with s the logistic function, z = g and
 // z = 2 sqrt(2/pi) (g + 0.044715 g^3) (as (1 + tanh(z/2)) / 2 = s(z)), and
-// f' = s + g s (1 - s) z'.  e = exp(-z) overflows to infinity for very
-// negative z, where s = 0 is right; 1 - s is taken as e s for z > 0, where the
-// subtraction would cancel.
+// f' = s + g s (1 - s) z'.  1 - s is taken as e s, e = exp(-z), for z > 0, where
+// the subtraction would cancel.
 //
 // GELU is g P(g) with P the normal distribution function:
 // P(-a) = exp(-a^2/2) t p(t), t = 1 / (1 + 0.32 a), a >= 0, with p a degree-7
 // polynomial fitted to exp(a^2/2) P(-a) / t for the least largest relative
 // error on [0, 60] (4.4e-7; 7.8e-7 with fp32 rounding), and P(a) = 1 - P(-a).  The
 // left tail keeps its relative accuracy.
-template <int FN, bool GRAD>
+//
+// The hardware exp2 and reciprocal flush subnormal results to zero, but f and f' there,
+// up to 2^-119, are bf16 values (f(-87.5) = -8.7e-37 for SiLU) and may be multiplied by a
+// large up.  So where exp(z) or exp(-g^2/2) nears 2^-126 in bf16, it is taken times 2^64 (for
+// s(z) it equals exp(z)), and 2^-64 comes last: below the normal range the result is
+// fp32's.  fp16 ends at 2^-25 and up at 2^16, where zero is right.
+template <int DT, int FN, bool GRAD>
 __device__ __forceinline__ void act_eval(float g, float& f, float& df) {
     if constexpr (FN == ZERO_GLU_GELU) {
         const float a = fabsf(g);
@@ -140,12 +145,18 @@ __device__ __forceinline__ void act_eval(float g, float& f, float& df) {
         p = __builtin_fmaf(p, t, 0x1.d0a53ep-4f);
         p = __builtin_fmaf(p, t, 0x1.05991ap-3f);
         p = __builtin_fmaf(p, t, 0x1.05728cp-3f);
-        const float e = exp2_hw(-0.5f * kLog2e * a * a);
+        const bool far = DT == ZERO_BF16 && g < -12.5f;
+        const float e = exp2_hw(__builtin_fmaf(-0.5f * kLog2e * a, a, far ? 64.0f : 0.0f));
         const float tail = e * (t * p);
         const float cdf = g > 0.0f ? 1.0f - tail : tail;
         f = g * cdf;
         // where the density is 0, 0 * g is 0 for every finite g
         if constexpr (GRAD) df = __builtin_fmaf(e * 0.3989422804014327f, g, cdf);
+        if constexpr (DT == ZERO_BF16) {
+            const float back = far ? 0x1p-64f : 1.0f;
+            f *= back;
+            if constexpr (GRAD) df *= back;
+        }
     } else {
         float z = g, zp = 1.0f, gc = g;
         if constexpr (FN == ZERO_GLU_GELU_TANH) {
@@ -155,14 +166,20 @@ __device__ __forceinline__ void act_eval(float g, float& f, float& df) {
             z = 1.5957691216057308f * gc * __builtin_fmaf(0.044715f, g2, 1.0f);
             zp = 1.5957691216057308f * __builtin_fmaf(0.134145f, g2, 1.0f);
         }
-        const float e = exp2_hw(-kLog2e * z);
-        const float s = rcp_hw(1.0f + e);
+        const bool far = DT == ZERO_BF16 && z < -80.0f;
+        const float e = exp2_hw(far ? __builtin_fmaf(kLog2e, z, 64.0f) : -kLog2e * z);
+        const float s = far ? e : rcp_hw(1.0f + e);
         f = g * s;
         if constexpr (GRAD) {
-            const float c = z > 0.0f ? e * s : 1.0f - s;
+            const float c = z > 0.0f ? e * s : 1.0f - s;  // (1 where far)
             df = s * __builtin_fmaf(gc * c, zp, 1.0f);
-            if constexpr (FN == ZERO_GLU_GELU_TANH) df += 0.0f * (g - gc);  // a NaN stays a NaN
         }
+        if constexpr (DT == ZERO_BF16) {
+            const float back = far ? 0x1p-64f : 1.0f;
+            f *= back;
+            if constexpr (GRAD) df *= back;
+        }
+        if constexpr (GRAD && FN == ZERO_GLU_GELU_TANH) df += 0.0f * (g - gc);  // a NaN stays a NaN
     }
 }
 
@@ -189,7 +206,7 @@ __global__ __launch_bounds__(kActThreads) void glu_forward_kernel(
 #pragma unroll
     for (int i = 0; i < kOct; ++i) {
         float f, df;
-        act_eval<FN, false>(g[i], f, df);
+        act_eval<DT, FN, false>(g[i], f, df);
         o[i] = GATED ? f * u[i] : f;
     }
     if (p.col < cols) store_oct(h + p.row * h_stride, p.col, cols, narrow_oct<DT>(o));
@@ -227,7 +244,7 @@ __global__ __launch_bounds__(kActThreads) void glu_backward_kernel(
 #pragma unroll
     for (int i = 0; i < kOct; ++i) {
         float f, df;
-        act_eval<FN, true>(g[i], f, df);
+        act_eval<DT, FN, true>(g[i], f, df);
         a[i] = (GATED ? d[i] * u[i] : d[i]) * df;
         b[i] = d[i] * f;
         o[i] = GATED ? f * u[i] : f;
