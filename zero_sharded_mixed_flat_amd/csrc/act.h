@@ -128,9 +128,9 @@ __device__ __forceinline__ float block_scale(const u4& w) {
 // correction q = q0 + (x - q0 scale) y give the IEEE quotient wherever the code
 // depends on its last bit: scale is A / qmax rounded, with A a 16-bit value
 // (an 11-bit significand at most), so x / scale = qmax x / A (1 + e),
-// |e| <= 2^-24, lies either further than 2^-13 (relative) from every rounding
-// boundary of the code or, but for e, on one; those finitely many cases are
-// compared exhaustively by the tests.  This is 3 operations instead of about 10
+// |e| <= 2^-24, lies either at least 2^-19 (relative; 2^-16 for bf16 or E4M3) from
+// every rounding boundary of the code or, but for e, on one; those finitely many
+// cases are compared exhaustively by the tests.  This is 3 operations instead of about 10
 // for a division, whose cost would exceed the memory time of the kernel.  Below
 // 2^-60 (reached by bf16 blocks of magnitudes under 1e-16 only) the residual may
 // leave the normal range and the division itself is used.  An INT8 code is the

@@ -124,8 +124,8 @@ __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(
 // GELU is g P(g) with P the normal distribution function:
 // P(-a) = exp(-a^2/2) t p(t), t = 1 / (1 + 0.32 a), a >= 0, with p a degree-7
 // polynomial fitted to exp(a^2/2) P(-a) / t for the least largest relative
-// error on [0, 60] (4.4e-7; 7.8e-7 with fp32 rounding), and P(a) = 1 - P(-a).  The
-// left tail keeps its relative accuracy.
+// error on [0, 60] (5.0e-7 with its coefficients in fp32, 8e-7 evaluated in fp32), and
+// P(a) = 1 - P(-a).  The left tail keeps its relative accuracy.
 //
 // The hardware exp2 and reciprocal flush subnormal results to zero, but f and f' there,
 // up to 2^-119, are bf16 values (f(-87.5) = -8.7e-37 for SiLU) and may be multiplied by a
