@@ -9,9 +9,9 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import act
-from test_gpu_act import FMT, TORCH16, Mat, _dev_ckpt, _note, abi  # noqa: F401
-from act_cases import activation
+from act_cases import activation, close16, wide
+from oracle import act, rounding
+from test_gpu_act import FMT, FN, TORCH16, Mat, _dev_ckpt, _note, abi  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,62 @@ def test_views_of_batches_and_heads(abi):
         abi.zero_act_save(flat.half(), cols, "bf16", rows, cols, 1, codes, scales)
     with pytest.raises(ValueError, match="torch.float64 values"):
         abi.zero_act_restore(codes, scales.double(), 1, rows, cols, y, 3 * cols, "bf16")
+
+
+@pytest.mark.parametrize("fn", ["silu", "gelu", "gelu_tanh"])
+def test_glu_gradients_against_differences(abi, fn):
+    # Gates and ups that the checkpoint holds exactly (multiples of 1/32 with a block maximum of 127/32), so the
+    # gradient is that of the forward pass; central differences of the oracle's forward pass in float64.
+    rng = np.random.default_rng(8)
+    rows, cols, step = 5, 60, 2.0 ** -5
+    g, u = (rng.integers(-126, 127, (rows, cols)) * step for _ in range(2))
+    g[:, 0] = u[:, 0] = 127 * step
+    bits = lambda v: rounding.narrow(v.astype(np.float32), "f16").reshape(rows, cols)
+    dh = activation(rng, rows, cols, "f16")
+    mg, mu, md = Mat(rows, cols, "f16", bits(g)), Mat(rows, cols, "f16", bits(u)), Mat(rows, cols, "f16", dh)
+    h, dg, du = Mat(rows, cols, "f16"), Mat(rows, cols, "f16"), Mat(rows, cols, "f16")
+    (gc, gs), (uc, us) = [(torch.empty(rows, 64, dtype=torch.uint8, device="cuda"), torch.empty(rows, 1, device="cuda"))
+                          for _ in range(2)]
+    abi.zero_act_glu_forward(mg.t, cols, mu.t, cols, "f16", rows, cols, FN[fn], 1, h.t, cols, gc, gs, uc, us)
+    abi.zero_act_glu_backward(gc, gs, uc, us, 1, rows, cols, FN[fn], md.t, cols, "f16", dg.t, cols, du.t, cols)
+    torch.cuda.synchronize()
+    assert bool((gs == step).all()) and bool((us == step).all())
+    d64, e = wide(dh, "f16"), 1e-4
+    f = lambda a, b: act.glu_forward(a, b, fn)[0] * d64          # element by element: differences of all at once
+    (_, ge), (_, ue), _ = act.glu_backward(g, u, d64, fn)
+    # truncation: e^2 / 6 |f'''| |u dh|, |f'''| below 1 for all three, |u| <= 4, |dh| < 64; rounding: a few ulps of
+    # |h dh| over e
+    slack = e * e / 6 * 4 * 64 + 2.0 ** -50 * 16 * 64 / e
+    close16(dg.bits(), (f(g + e, u) - f(g - e, u)) / (2 * e), ge + slack, "f16", "dgate")
+    close16(du.bits(), (f(g, u + e) - f(g, u - e)) / (2 * e), ue + slack, "f16", "dup")
+
+
+def test_weight_gradient_against_differences(abi):
+    # The loss sum(dy (x W^T + b)) is linear in W and b: differences of any width are its gradient.
+    rng = np.random.default_rng(4)
+    rows, inner, outer = 9, 20, 7
+    x = rng.integers(-60, 61, (rows, inner)).astype(np.float64)
+    x[:, 0] = 127
+    xb = rounding.narrow(x.astype(np.float32), "bf16").reshape(rows, inner)
+    dy = activation(rng, rows, outer, "bf16")
+    codes, scales = _dev_ckpt(*act.save(xb, "bf16", "int8"))
+    md, mw, mb = Mat(rows, outer, "bf16", dy), Mat(outer, inner, "bf16"), Mat(1, outer, "bf16")
+    abi.zero_act_weight_grad(md.t, outer, "bf16", codes, scales, 1, rows, inner, outer, False, mw.t, mb.t, None,
+                             workspace_bytes=0)
+    torch.cuda.synchronize()
+    d64, w, b = wide(dy, "bf16"), rng.standard_normal((outer, inner)), rng.standard_normal(outer)
+    loss = lambda w, b: (d64 * (x @ w.T + b)).sum()
+    num, numb = np.zeros_like(w), np.zeros_like(b)
+    for o in range(outer):
+        for i in range(inner):
+            p = np.zeros_like(w)
+            p[o, i] = 1.0
+            num[o, i] = (loss(w + p, b) - loss(w - p, b)) / 2
+        q = np.zeros_like(b)
+        q[o] = 1.0
+        numb[o] = (loss(w, b + q) - loss(w, b - q)) / 2
+    (_, we), (_, be) = act.weight_grad(d64, x)
+    # float64 losses of sums of 9 * 7 * 20 products of up to 127 * 8 * 4
+    slack = 2.0 ** -52 * 9 * 7 * 20 * 127 * 8 * 4
+    close16(mw.bits(), num, we + slack, "bf16", "dweight")
+    close16(mb.bits()[0], numb, be + slack, "bf16", "dbias")
