@@ -517,11 +517,13 @@ int zero_gather_dequant(const zero_plan* plan, const void* const* code_shards,
  *                  even in 4 exponent and 3 mantissa bits (largest value 448,
  *                  no infinities), clamped to [-448, 448]
  * with IEEE fp32 divisions.  Restored value = round_to_nearest_even_16(fp32(
- * code * scale)); a backward pass computes with these 16-bit values, so it
- * gives what the ordinary backward pass gives on the restored activation.  A
- * block of zeros has scale 0.  A block that holds an infinity or NaN has scale
- * NaN and codes 0: all of it is restored as NaN, so a non-finite activation
- * reaches the gradient and its flag instead of turning finite.
+ * code * scale)); a backward pass computes with these 16-bit values.  For the
+ * gated activation and the weight gradient that is the ordinary backward pass
+ * on the restored activation; the norm's takes the restored row together with
+ * the mean and rstd of the row as it was before the checkpoint.  A block of
+ * zeros has scale 0.  A block that holds an infinity or NaN has scale NaN and
+ * codes 0: all of it is restored as NaN, so a non-finite activation reaches the
+ * gradient and its flag instead of turning finite.
  *
  * Layout: codes, one byte per element, rows ceil(cols / 16) * 16 bytes apart
  * (the pad bytes are written as 0), 16-byte aligned; scales, fp32,
@@ -534,12 +536,14 @@ int zero_gather_dequant(const zero_plan* plan, const void* const* code_shards,
  * aligned; columns are adjacent.  Two matrices of one call with the same
  * stride may interleave (the halves of one product's output); otherwise
  * outputs may not overlap each other or an input (ZERO_EALIAS), except where a
- * call says so.  `dtype` is that of every 16-bit array of the call.
+ * call says so.  What lies between an input's rows may be read; its values do
+ * not matter.  Between an output's rows nothing is written.  `dtype` is that of every 16-bit array of the call.
  * 0 <= rows, 0 <= cols <= ZERO_ACT_MAX_COLS, and rows * (cols rounded up to
  * ZERO_QBLOCK) <= ZERO_MAX_ELEMS.  With no rows or no columns the arrays that
  * then hold nothing may be NULL or not, also where a call says which go
- * together.  Sums are fp32 in an order that depends only on the sizes,
- * so results are bitwise repeatable.  Nothing is allocated, copied to the
+ * together.  Sums are fp32 in an order that depends only on the sizes
+ * (a bias gradient's also on whether dy_stride lies within 8 .. 2^24 - 1), so
+ * results are bitwise repeatable.  Nothing is allocated, copied to the
  * host or recorded as a memset: every call can be captured in a HIP graph.
  */
 #define ZERO_ACT_INT8 1
@@ -881,7 +885,10 @@ int zero_cpu_set_isa(int isa);
 /* Message for the last error on the calling thread ("" if none). */
 const char* zero_last_error(void);
 
-/* ABI version: major * 10000 + minor * 100 + patch. */
+/* ABI version: major * 10000 + minor * 100 + patch.  Libraries of version
+ * 10301 exist with and without the activation calls: a header that has them
+ * defines ZERO_ACT_INT8, a library loaded at run time that has them exports
+ * zero_act_save. */
 int zero_version(void);
 
 #ifdef __cplusplus

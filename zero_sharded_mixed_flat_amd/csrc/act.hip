@@ -183,7 +183,8 @@ __device__ __forceinline__ void act_eval(float g, float& f, float& df) {
     }
 }
 
-// One pair of blocks per wave: 8192 x 16384 gated forward 171 us, with 2 180, with 4 186.
+// One pair of blocks per wave: 8192 x 16384 gated forward 174 us (with 2 it took 9 us more,
+// with 4 15).
 template <int DT, int FMT, int FN, bool GATED>
 __global__ __launch_bounds__(kActThreads) void glu_forward_kernel(
     const uint16_t* __restrict__ gate, int64_t gate_stride, const uint16_t* __restrict__ up, int64_t up_stride,
@@ -220,7 +221,7 @@ __global__ __launch_bounds__(kActThreads) void glu_forward_kernel(
     }
 }
 
-// Bound by memory too (8192 x 16384 gated with h: 216 us, 6.3 TB/s): about 50 operations per
+// Bound by memory too (8192 x 16384 gated with h: 212 us, 6.3 TB/s): about 50 operations per
 // element hide behind 10 bytes.
 template <int DT, int FMT, int FN, bool GATED>
 __global__ __launch_bounds__(kActThreads) void glu_backward_kernel(
@@ -265,7 +266,8 @@ __global__ __launch_bounds__(kActThreads) void glu_backward_kernel(
 // two passes over the registers (mean, then squared distances), which costs no
 // memory time: 16384 x 4096 with a branch, 101 us and 6.0 TB/s forward, 123 us
 // backward with both parameter gradients (4.9 TB/s: the row's two sums stand
-// between its loads and its stores).
+// between its loads and its stores).  The backward pass of more than 8192 columns (two
+// octs per thread at 1024 threads) keeps 9 registers in scratch memory.
 template <int T>
 constexpr int norm_rows() {
     return T >= 256 ? 1 : 256 / T;

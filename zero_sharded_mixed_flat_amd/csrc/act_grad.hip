@@ -13,11 +13,13 @@
 // decoded on their way into LDS, between the matrix instructions of the previous
 // tile, or for large products beforehand, once for all blocks.
 //
-// Large products are bound by power: the matrix units are busy 58% of the cycles
-// (32 x 32 x 16 version) and the clock settles near 1.5 GHz, so what counts is
-// the energy around the products.  16384 tokens, 4096 -> 16384 in bf16: 1690 us,
-// 1300 TFLOP/s, where 16384^3 by the library reaches 1592 and the library's product
-// of this shape (both operands transposed in memory) takes 1819 us.
+// Large products: 16384 tokens, 4096 -> 16384 in bf16 take 1610-1680 us, 1310-1370
+// TFLOP/s, where 16384^3 by the library reaches 1584 and the library's product of this
+// shape (both operands transposed in memory) takes 1820-1860 us.  Two things bound it.
+// At the full clock of 2.1 GHz the matrix units are busy 60% of the cycles: one wave per
+// SIMD issues everything else between its own matrix instructions.  Over a run of such
+// calls the clock falls to 1.65-1.9 GHz with the power drawn and the share rises to
+// 66-68%, so the energy around the products counts too.
 
 #include "act.h"
 
@@ -78,8 +80,8 @@ struct GradArgs {
 // Order of a step's instructions: after every two matrix instructions, which keep
 // the matrix unit busy for 8 issue slots, its share of the LDS reads (one of 32 at
 // 256 x 256, two of 16 at 128 x 128) and a few of the others, so that a lone wave per
-// SIMD does not leave it idle.  Without it 16384 tokens, 4096 -> 16384, take 1900
-// instead of 1716 us.
+// SIMD does not leave it idle.  Without it 16384 tokens, 4096 -> 16384, take 1907
+// instead of 1613 us and 4096 tokens, 1600 -> 6400, 113 instead of 105.
 template <int F, int VALU>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
@@ -338,7 +340,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, char* smem, int o0,
 // Blocks are dispatched round-robin to the 8 XCDs; each XCD takes a contiguous
 // run of tiles, ordered so that the 32 tiles in flight (one per CU) form a patch of
 // 4 output tiles by 8 input tiles that share operand panels in its L2 (8 by 4 was
-// 1.5% slower at 16384 tokens, 4096 -> 16384).
+// 4% slower at 16384 tokens, 4096 -> 16384).
 __device__ __forceinline__ void place_tile(int id, int count, int out_tiles, int in_tiles, int& o, int& i) {
     constexpr int kXcds = 8, kGroup = 4;
     const int per = count / kXcds, extra = count % kXcds;
@@ -363,8 +365,10 @@ __global__ __launch_bounds__(kGradThreads) void weight_grad_kernel(GradArgs g) {
     const int o0 = ot * TILE, i0 = in * TILE;
     const int64_t t0 = split * g.split_rows;
     const int64_t t_end = t0 + g.split_rows < g.rows ? t0 + g.split_rows : g.rows;
-    // TILE 256 is launched for unchecked calls in one split of at least 128 tokens only:
-    // a checked loop there would spill registers and cost every launch its scratch memory.
+    // TILE 256 is launched for unchecked calls in one split of at least 128 tokens only.
+    // 256 accumulators and two sets of fragments and loads leave 9 or 10 registers of its
+    // loop in scratch memory (40 or 44 bytes per lane); with a checked loop beside it the
+    // kernel kept 157 to 229 there.
     if (TILE == 128 && !(g.unchecked && t_end - t0 >= kUncheckedTokens)) {
         if constexpr (TILE == 128) grad_tile<DT, FMT, TILE, kGuarded, true>(g, smem, o0, i0, t0, t_end, split);
     } else if (g.dbias != nullptr && in == 0) {
@@ -426,11 +430,11 @@ constexpr int kCus = 256;
 // Restoring the input first costs a launch (3 us) and 3 bytes per element, and saves
 // every output tile the decoding, which draws issue slots and power from the matrix
 // units.  Measured without and with (us), INT8:
-//   256 x 256 tiles  16384 tokens 4096 -> 16384 1994 / 1716; 16384 tokens 16384 -> 2048
-//                    952 / 959, -> 1024 523 / 566; 2048 tokens 4096 -> 4096 69 / 68;
-//                    512 tokens 4096 -> 4096 28 / 31
-//   128 x 128 tiles  4096 tokens 1600 -> 6400 135 / 116, 6400 -> 1600 135 / 127; 16384
-//                    tokens 2048 -> 1024 97 / 113; 48 tokens 1600 -> 4800 9 / 11
+//   256 x 256 tiles  16384 tokens 4096 -> 16384 1839 / 1631; 16384 tokens 16384 -> 2048
+//                    898 / 917, -> 1024 456 / 526; 2048 tokens 4096 -> 4096 64 / 64;
+//                    512 tokens 4096 -> 4096 24 / 28
+//   128 x 128 tiles  4096 tokens 1600 -> 6400 120 / 105, 6400 -> 1600 120 / 116; 16384
+//                    tokens 2048 -> 1024 89 / 109; 48 tokens 1600 -> 4800 8 / 10
 constexpr int64_t kDecodeOutputs = 1536;       // with 128 x 128 tiles
 constexpr int64_t kDecodeOutputsLarge = 2048;  // with 256 x 256 tiles, which decode half as often
 constexpr int64_t kDecodeProducts = 10000000000;
@@ -440,8 +444,8 @@ inline GradShape grad_shape(int64_t rows, int64_t in_cols, int64_t out_cols) {
         return std::max<int64_t>(1, ceil_div(in_cols, int64_t(tile))) * ceil_div(out_cols, int64_t(tile));
     };
     GradShape s;
-    // 256 x 256 tiles where they give every CU one (128 x 128 tiles take 2257 instead of 1716
-    // us for 16384 tokens, 4096 -> 16384; 256 x 256 ones 157 instead of 117 us for 4096 tokens,
+    // 256 x 256 tiles where they give every CU one (128 x 128 tiles take 2124 instead of 1613
+    // us for 16384 tokens, 4096 -> 16384; 256 x 256 ones 143 instead of 105 us for 4096 tokens,
     // 1600 -> 6400) and the unchecked loop runs.
     s.tile = rows >= kUncheckedTokens && tiles(256) >= kCus ? 256 : 128;
     s.in_tiles = int(std::max<int64_t>(1, ceil_div(in_cols, int64_t(s.tile))));
