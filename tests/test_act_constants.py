@@ -19,7 +19,7 @@ def _tail_polynomial():
     """(0.32, coefficients from t^7 down to t^0) as written in act.hip."""
     with open(os.path.join(CSRC, "act.hip")) as f:
         text = f.read()
-    body = text[text.index("FN == ZERO_GLU_GELU)"):text.index("const float tail")]
+    body = text[text.index("float normal_tail(float a) {"):text.index("return t * p;")]
     rate = float(re.search(r"fmaf\((0\.\d+)f, a, 1\.0f\)", body).group(1))
     coef = [float.fromhex(c) for c in re.findall(r"-?0x1\.[0-9a-f]+p[-+]\d+", body)]
     assert len(coef) == 8

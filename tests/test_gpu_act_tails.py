@@ -86,3 +86,48 @@ def test_the_ordinary_range_meets_the_tail(abi, fn):
     torch.cuda.synchronize()
     v, e = act.glu_forward(wide(x, "bf16"), None, fn)
     _near(h.bits(), v, WIDER[fn] * e + 2.0 ** -150, "h")
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("fn", sorted(FN))
+def test_blocks_that_mix_tail_and_ordinary_values(abi, fn, fmt):
+    # Octs with and without tail values, blocks whose largest magnitude is a positive value, a value just at the
+    # tail's border, and one with a NaN, whose other values keep their own activation.
+    rng = np.random.default_rng(5)
+    rows, cols = 24, 530
+    hi, lo = RANGE[fn]
+    x = np.where(rng.random((rows, cols)) < 0.1, rng.uniform(lo, hi / 2, (rows, cols)), rng.standard_normal((rows, cols)))
+    x[3] = np.abs(x[3])
+    x[4] = hi * 0.98
+    x[5, ::8] = -lo
+    bits = rounding.narrow(x.astype(np.float32), "bf16").reshape(rows, cols)
+    bits[7, 100] = 0xFFC0                            # a NaN with its sign set
+    bits[8, 300] = 0xFF80                            # minus infinity
+    u = rounding.narrow((rng.standard_normal((rows, cols)) * 2.0 ** 60).astype(np.float32), "bf16").reshape(rows, cols)
+    fm = {"int8": 1, "e4m3": 2}[fmt]
+    m, mu, h = Mat(rows, cols, "bf16", bits), Mat(rows, cols, "bf16", u), Mat(rows, cols, "bf16", pad=3)
+    (gc, gs), (uc, us) = _ckpt(abi, rows, cols), _ckpt(abi, rows, cols)
+    abi.zero_act_glu_forward(m.t, cols, mu.t, cols, "bf16", rows, cols, FN[fn], fm, h.t, h.stride, gc, gs, uc, us)
+    dh = rounding.narrow(rng.standard_normal((rows, cols)).astype(np.float32), "bf16").reshape(rows, cols)
+    d, dg, du = Mat(rows, cols, "bf16", dh), Mat(rows, cols, "bf16"), Mat(rows, cols, "bf16")
+    abi.zero_act_glu_backward(gc, gs, uc, us, fm, rows, cols, FN[fn], d.t, cols, "bf16", dg.t, cols, du.t, cols)
+    torch.cuda.synchronize()
+    k, least = WIDER[fn], 2.0 ** -150
+    bad = np.zeros((rows, cols), bool)
+    bad[7, 100] = bad[8, 300] = True
+    g, uu = wide(np.where(bad, 0, bits).astype(np.uint16), "bf16"), wide(u, "bf16")
+    v, e = act.glu_forward(g, uu, fn)
+    got = h.bits()
+    assert np.isnan(wide(got, "bf16")[bad]).all()
+    _near(got[~bad], v[~bad], (k * e + (np.abs(uu) + 1) * least)[~bad], "h")
+    rg = wide(act.restore(*act.save(bits, "bf16", fmt), "bf16", fmt), "bf16")
+    ru = wide(act.restore(*act.save(u, "bf16", fmt), "bf16", fmt), "bf16")
+    nan = np.isnan(rg)
+    assert nan[7, :256].all() and nan[8, 256:512].all() and nan.sum() == 512
+    d64 = wide(dh, "bf16")
+    (a, ae), (b, be), _ = act.glu_backward(np.where(nan, 0, rg), ru, d64, fn)
+    for out, want, err, what in ((dg, a, k * ae + (np.abs(d64 * ru) + 1) * least, "dgate"),
+                                 (du, b, k * be + (np.abs(d64) + 1) * least, "dup")):
+        assert np.isnan(wide(out.bits(), "bf16")[nan]).all()
+        _near(out.bits()[~nan], want[~nan], err[~nan], what)
+    assert h.guards_intact()

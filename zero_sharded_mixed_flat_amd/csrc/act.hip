@@ -113,6 +113,30 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
 
+// exp(a^2/2) P(-a) for a >= 0, with P the normal distribution function: t p(t),
+// t = 1 / (1 + 0.32 a), with p a degree-7 polynomial fitted to it over t for the
+// least largest relative error on [0, 60] (5.0e-7 with its coefficients in fp32, 8e-7
+// evaluated in fp32).
+__device__ __forceinline__ float normal_tail(float a) {
+    const float t = rcp_hw(__builtin_fmaf(0.32f, a, 1.0f));
+    float p = 0x1.1acb3cp-5f;
+    p = __builtin_fmaf(p, t, -0x1.f57a54p-4f);
+    p = __builtin_fmaf(p, t, 0x1.b2a5c6p-4f);
+    p = __builtin_fmaf(p, t, 0x1.fed612p-7f);
+    p = __builtin_fmaf(p, t, 0x1.8ed7dap-4f);
+    p = __builtin_fmaf(p, t, 0x1.d0a53ep-4f);
+    p = __builtin_fmaf(p, t, 0x1.05991ap-3f);
+    p = __builtin_fmaf(p, t, 0x1.05728cp-3f);
+    return t * p;
+}
+
+// The tanh form's z and z' of a g within [-30, 30].
+__device__ __forceinline__ void tanh_arg(float g, float& z, float& zp) {
+    const float g2 = g * g;
+    z = 1.5957691216057308f * g * __builtin_fmaf(0.044715f, g2, 1.0f);
+    zp = 1.5957691216057308f * __builtin_fmaf(0.134145f, g2, 1.0f);
+}
+
 // f(g) and, with GRAD, f'(g) in fp32.  The hardware exp2 and reciprocal are
 // good to about an fp32 ulp; every result is rounded to 16 bits next.
 //
@@ -121,69 +145,84 @@ __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(
 // f' = s + g s (1 - s) z'.  1 - s is taken as e s, e = exp(-z), for z > 0, where
 // the subtraction would cancel.
 //
-// GELU is g P(g) with P the normal distribution function:
-// P(-a) = exp(-a^2/2) t p(t), t = 1 / (1 + 0.32 a), a >= 0, with p a degree-7
-// polynomial fitted to exp(a^2/2) P(-a) / t for the least largest relative
-// error on [0, 60] (5.0e-7 with its coefficients in fp32, 8e-7 evaluated in fp32), and
-// P(a) = 1 - P(-a).  The left tail keeps its relative accuracy.
-//
-// The hardware exp2 and reciprocal flush subnormal results to zero, but f and f' there,
-// up to 2^-119, are bf16 values (f(-87.5) = -8.7e-37 for SiLU) and may be multiplied by a
-// large up.  So where exp(z) or exp(-g^2/2) nears 2^-126 in bf16, it is taken times 2^64 (for
-// s(z) it equals exp(z)), and 2^-64 comes last: below the normal range the result is
-// fp32's.  fp16 ends at 2^-25 and up at 2^16, where zero is right.
-template <int DT, int FN, bool GRAD>
+// GELU is g P(g), P(-a) = exp(-a^2/2) normal_tail(a) for a >= 0 and P(a) = 1 - P(-a).
+// The left tail keeps its relative accuracy.
+template <int FN, bool GRAD>
 __device__ __forceinline__ void act_eval(float g, float& f, float& df) {
     if constexpr (FN == ZERO_GLU_GELU) {
         const float a = fabsf(g);
-        const float t = rcp_hw(__builtin_fmaf(0.32f, a, 1.0f));
-        float p = 0x1.1acb3cp-5f;
-        p = __builtin_fmaf(p, t, -0x1.f57a54p-4f);
-        p = __builtin_fmaf(p, t, 0x1.b2a5c6p-4f);
-        p = __builtin_fmaf(p, t, 0x1.fed612p-7f);
-        p = __builtin_fmaf(p, t, 0x1.8ed7dap-4f);
-        p = __builtin_fmaf(p, t, 0x1.d0a53ep-4f);
-        p = __builtin_fmaf(p, t, 0x1.05991ap-3f);
-        p = __builtin_fmaf(p, t, 0x1.05728cp-3f);
-        const bool far = DT == ZERO_BF16 && g < -12.5f;
-        const float e = exp2_hw(__builtin_fmaf(-0.5f * kLog2e * a, a, far ? 64.0f : 0.0f));
-        const float tail = e * (t * p);
+        const float e = exp2_hw(-0.5f * kLog2e * a * a);
+        const float tail = e * normal_tail(a);
         const float cdf = g > 0.0f ? 1.0f - tail : tail;
         f = g * cdf;
         // where the density is 0, 0 * g is 0 for every finite g
         if constexpr (GRAD) df = __builtin_fmaf(e * 0.3989422804014327f, g, cdf);
-        if constexpr (DT == ZERO_BF16) {
-            const float back = far ? 0x1p-64f : 1.0f;
-            f *= back;
-            if constexpr (GRAD) df *= back;
-        }
     } else {
         float z = g, zp = 1.0f, gc = g;
         if constexpr (FN == ZERO_GLU_GELU_TANH) {
             // beyond |g| = 30, s is 0 or 1 in fp32; clamping keeps g^2 and z' finite
             gc = fminf(fmaxf(g, -30.0f), 30.0f);
-            const float g2 = gc * gc;
-            z = 1.5957691216057308f * gc * __builtin_fmaf(0.044715f, g2, 1.0f);
-            zp = 1.5957691216057308f * __builtin_fmaf(0.134145f, g2, 1.0f);
+            tanh_arg(gc, z, zp);
         }
-        const bool far = DT == ZERO_BF16 && z < -80.0f;
-        const float e = exp2_hw(far ? __builtin_fmaf(kLog2e, z, 64.0f) : -kLog2e * z);
-        const float s = far ? e : rcp_hw(1.0f + e);
+        const float e = exp2_hw(-kLog2e * z);
+        const float s = rcp_hw(1.0f + e);
         f = g * s;
         if constexpr (GRAD) {
-            const float c = z > 0.0f ? e * s : 1.0f - s;  // (1 where far)
+            const float c = z > 0.0f ? e * s : 1.0f - s;
             df = s * __builtin_fmaf(gc * c, zp, 1.0f);
+            if constexpr (FN == ZERO_GLU_GELU_TANH) df += 0.0f * (g - gc);  // a NaN stays a NaN
         }
-        if constexpr (DT == ZERO_BF16) {
-            const float back = far ? 0x1p-64f : 1.0f;
-            f *= back;
-            if constexpr (GRAD) df *= back;
-        }
-        if constexpr (GRAD && FN == ZERO_GLU_GELU_TANH) df += 0.0f * (g - gc);  // a NaN stays a NaN
     }
 }
 
-// One pair of blocks per wave: 8192 x 16384 gated forward 174 us (with 2 it took 9 us more,
+// The far left tail.  The hardware exp2 and reciprocal flush subnormal results to zero,
+// but f and f' there, up to 2^-119, are bf16 values (f(-87.5) = -8.7e-37 for SiLU) and may be
+// multiplied by a large up.  So below kFar (z below -78, or the density near 2^-113) exp(z) or
+// exp(-g^2/2) is taken times 2^64 (s(z) equals exp(z) there, and 1 - s is 1), and 2^-64 comes
+// last: under the normal range the result is fp32's.  fp16 ends at 2^-25 and up at 2^16,
+// where zero is right.
+template <int FN>
+constexpr float kFar = FN == ZERO_GLU_SILU ? -80.0f : FN == ZERO_GLU_GELU ? -12.5f : -9.625f;
+
+template <int FN, bool GRAD>
+__device__ __forceinline__ void act_tail(float g, float& f, float& df) {
+    if constexpr (FN == ZERO_GLU_GELU) {
+        const float a = -g;
+        const float e = exp2_hw(__builtin_fmaf(-0.5f * kLog2e * a, a, 64.0f));
+        const float tail = e * normal_tail(a);
+        f = g * tail * 0x1p-64f;
+        if constexpr (GRAD) df = __builtin_fmaf(e * 0.3989422804014327f, g, tail) * 0x1p-64f;
+    } else {
+        float z = g, zp = 1.0f, gc = g;
+        if constexpr (FN == ZERO_GLU_GELU_TANH) {
+            gc = fmaxf(g, -30.0f);
+            tanh_arg(gc, z, zp);
+        }
+        const float s = exp2_hw(__builtin_fmaf(kLog2e, z, 64.0f));
+        f = g * s * 0x1p-64f;
+        if constexpr (GRAD) {
+            df = s * __builtin_fmaf(gc, zp, 1.0f) * 0x1p-64f;
+            if constexpr (FN == ZERO_GLU_GELU_TANH) df += 0.0f * (g - gc);
+        }
+    }
+}
+
+// Whether an oct of 16-bit patterns has a value below kFar.  Its block's scale rules most
+// out (not where it is NaN; a hundredth covers its roundings).  Patterns of negative values
+// order like their magnitudes and lie above those of positive ones, so one integer maximum
+// tells the rest (or finds a NaN, which is then not below kFar).  Ordinary data has none, so
+// the tail stands behind a branch: computed for every element and selected, it made 262 x 9
+// 9% and 8192 x 16384 up to 9% slower.  Branched over, it costs the GELU forms' forward pass
+// 1 to 3% at 8192 x 16384 and a few hundredths of a microsecond elsewhere.
+template <int DT, int FMT, int FN>
+__device__ __forceinline__ bool any_far(const u4& w, float scale) {
+    if (DT != ZERO_BF16 || scale < -0.99f * kFar<FN> / act_qmax<FMT>()) return false;
+    constexpr uint32_t far = __builtin_bit_cast(uint32_t, kFar<FN>) >> 16;
+    const uint32_t m = max_pair(max_pair(w[0], w[1]), max_pair(w[2], w[3]));
+    return max(m & 0xffffu, m >> 16) > far;
+}
+
+// One pair of blocks per wave: 8192 x 16384 gated forward 172 us (with 2 it took 9 us more,
 // with 4 15).
 template <int DT, int FMT, int FN, bool GATED>
 __global__ __launch_bounds__(kActThreads) void glu_forward_kernel(
@@ -204,11 +243,25 @@ __global__ __launch_bounds__(kActThreads) void glu_forward_kernel(
     float g[kOct], u[kOct], o[kOct];
     widen_oct<DT>(wg, g);
     if constexpr (GATED) widen_oct<DT>(wu, u);
+    const auto value = [&](int i, float f) { o[i] = GATED ? f * u[i] : f; };
 #pragma unroll
     for (int i = 0; i < kOct; ++i) {
         float f, df;
-        act_eval<DT, FN, false>(g[i], f, df);
-        o[i] = GATED ? f * u[i] : f;
+        act_eval<FN, false>(g[i], f, df);
+        value(i, f);
+    }
+    // in one piece with f: behind the branch, 262 x 9 took 4.1 us instead of 3.7
+    const u2 cg = encode_oct<FMT>(g, gs);
+    u2 cu{0u, 0u};
+    if constexpr (GATED) cu = encode_oct<FMT>(u, us);
+    if (any_far<DT, FMT, FN>(wg, gs)) {
+#pragma unroll
+        for (int i = 0; i < kOct; ++i) {
+            if (!(g[i] < kFar<FN>)) continue;
+            float f, df;
+            act_tail<FN, false>(g[i], f, df);
+            value(i, f);
+        }
     }
     if (p.col < cols) store_oct(h + p.row * h_stride, p.col, cols, narrow_oct<DT>(o));
     if ((threadIdx.x & 31) == 0) {
@@ -216,8 +269,8 @@ __global__ __launch_bounds__(kActThreads) void glu_forward_kernel(
         if constexpr (GATED) up_scales[p.block] = us;
     }
     if (p.col < pitch) {
-        store_codes(gate_codes + p.row * pitch, p.col, encode_oct<FMT>(g, gs));
-        if constexpr (GATED) store_codes(up_codes + p.row * pitch, p.col, encode_oct<FMT>(u, us));
+        store_codes(gate_codes + p.row * pitch, p.col, cg);
+        if constexpr (GATED) store_codes(up_codes + p.row * pitch, p.col, cu);
     }
 }
 
@@ -235,20 +288,26 @@ __global__ __launch_bounds__(kActThreads) void glu_backward_kernel(
     const u4 wd = load_oct(dh + p.row * dh_stride, p.col, cols);
     const u2 qg = load_codes(gate_codes + p.row * pitch, p.col);
     const float sg = gate_scales[p.block];
-    float d[kOct], g[kOct], u[kOct], a[kOct], b[kOct], o[kOct];
+    float d[kOct], g[kOct], u[kOct], f[kOct], df[kOct], a[kOct], b[kOct], o[kOct];
     if constexpr (GATED) {
         const u2 qu = load_codes(up_codes + p.row * pitch, p.col);
         widen_oct<DT>(decode_oct<DT, FMT>(qu, up_scales[p.block]), u);
     }
     widen_oct<DT>(wd, d);
-    widen_oct<DT>(decode_oct<DT, FMT>(qg, sg), g);
+    const u4 wg = decode_oct<DT, FMT>(qg, sg);
+    widen_oct<DT>(wg, g);
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) act_eval<FN, true>(g[i], f[i], df[i]);
+    if (any_far<DT, FMT, FN>(wg, sg)) {
+#pragma unroll
+        for (int i = 0; i < kOct; ++i)
+            if (g[i] < kFar<FN>) act_tail<FN, true>(g[i], f[i], df[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kOct; ++i) {
-        float f, df;
-        act_eval<DT, FN, true>(g[i], f, df);
-        a[i] = (GATED ? d[i] * u[i] : d[i]) * df;
-        b[i] = d[i] * f;
-        o[i] = GATED ? f * u[i] : f;
+        a[i] = (GATED ? d[i] * u[i] : d[i]) * df[i];
+        b[i] = d[i] * f[i];
+        o[i] = GATED ? f[i] * u[i] : f[i];
     }
     store_oct(dgate + p.row * dgate_stride, p.col, cols, narrow_oct<DT>(a));
     if constexpr (GATED) store_oct(dup + p.row * dup_stride, p.col, cols, narrow_oct<DT>(b));
