@@ -16,9 +16,9 @@
 // Large products: 16384 tokens, 4096 -> 16384 in bf16 take 1610-1680 us, 1310-1370
 // TFLOP/s, where 16384^3 by the library reaches 1584 and the library's product of this
 // shape (both operands transposed in memory) takes 1820-1860 us.  Two things bound it.
-// At the full clock of 2.1 GHz the matrix units are busy 60% of the cycles: one wave per
-// SIMD issues everything else between its own matrix instructions.  Over a run of such
-// calls the clock falls to 1.65-1.9 GHz with the power drawn and the share rises to
+// At the full clock of 2.1 GHz the matrix units are busy 60-62% of the cycles: one wave
+// per SIMD issues everything else between its own matrix instructions.  Over a run of such
+// calls the clock falls to 1.6-1.9 GHz with the power drawn and the share rises to
 // 66-68%, so the energy around the products counts too.
 
 #include "act.h"
